@@ -64,10 +64,12 @@ typedef enum kda_status {
   KDA_ERR_DTYPE = 7,       /* a tensor has the wrong dtype */
   KDA_ERR_STRIDE = 8,      /* a tensor's strides are not supported (see kda_fwd) */
   KDA_ERR_DEVICE = 9,      /* kda_device_status: the device recorded a fault */
-  KDA_ERR_VALUE = 10       /* a scalar argument is outside its range */
+  KDA_ERR_VALUE = 10,      /* a scalar argument is outside its range */
+  KDA_ERR_OVERLAP = 11     /* kda_conv_*, kda_ssm_*: an output overlaps an input
+                              or another output */
 } kda_status_t;
 
-typedef enum kda_dtype { KDA_BF16 = 1, KDA_F32 = 2, KDA_I32 = 3 } kda_dtype_t;
+typedef enum kda_dtype { KDA_BF16 = 1, KDA_F32 = 2, KDA_I32 = 3, KDA_F16 = 4 } kda_dtype_t;
 
 /*
  * A strided tensor in device memory. shape[0..ndim) and stride[0..ndim) are
@@ -333,6 +335,127 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
                      const kda_tensor_t* dg, const kda_tensor_t* dbeta,
                      const kda_tensor_t* dinitial_state, void* stream);
 
+/*
+ * The short causal convolution: a depthwise convolution over the tokens of each
+ * sequence with W taps (2 to 4), the step in front of the recurrence in layers
+ * of this kind (for KDA on q, k and v, before kda_fwd_fused). Per channel c:
+ *
+ *   p_t = bias[c] + sum_j weight[c, j] x_{t-W+1+j},   y_t = p_t or p_t sigmoid(p_t)
+ *
+ * The inputs before a sequence's first token are its state, W - 1 rows, oldest
+ * first (zeros without one); the state after a sequence is its last W - 1
+ * inputs, so a prompt can be taken in pieces and continued token by token.
+ *
+ * Shared by kda_conv_* and kda_ssm_*
+ *   - Token tensors are bf16, fp16 or fp32 (all of a call the same), parameters
+ *     fp32, sums fp32, each result rounded once. Token tensors may have any
+ *     positive token (and group) strides and need only their element's
+ *     alignment; the last dimension must have stride 1. Rows of 16-byte
+ *     alignment and stride are read 16 bytes at a time. The other tensors are
+ *     contiguous.
+ *   - cu_seqlens as for kda_fwd, except that cu[N] may be less than T (a padded
+ *     batch): the tokens behind the last sequence are not read, their outputs
+ *     are left as they were and their gradients are zero. Zero-length sequences
+ *     and T = 0 are allowed. Violations are recorded in the device status word.
+ *   - An output may not overlap an input or another output (KDA_ERR_OVERLAP)
+ *     unless the call says so.
+ *   - Results are deterministic: no atomics on data. kda_conv_bwd and
+ *     kda_ssm_bwd take scratch from the library's pool, the others none.
+ *   - Calls can be captured into CUDA graphs and run on any stream.
+ */
+#define KDA_ACT_NONE 0
+#define KDA_ACT_SILU 1
+
+/*
+ * kda_conv_fwd -- the convolution of a packed batch.
+ *   x, out          [T, C]      C <= 2^20
+ *   weight          fp32 [C, W]; bias fp32 [C] or NULL
+ *   activation      KDA_ACT_NONE or KDA_ACT_SILU, else KDA_ERR_VALUE
+ *   initial_state   [N, W - 1, C] of x's type, or NULL (zeros)
+ *   final_state     the same, or NULL (not written)
+ */
+kda_status_t kda_conv_fwd(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias,
+                          int32_t activation, const int32_t* cu_seqlens, int32_t num_seqs,
+                          const kda_tensor_t* initial_state, const kda_tensor_t* out,
+                          const kda_tensor_t* final_state, void* stream);
+
+/*
+ * kda_conv_decode -- one token of each of B requests.
+ *   x, out          [B, C]; out may be x itself
+ *   state           [P, W - 1, C] of x's type, read and written in place
+ *   state_indices   as for kda_decode
+ */
+kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias,
+                             int32_t activation, const kda_tensor_t* state, const int32_t* state_indices,
+                             const kda_tensor_t* out, void* stream);
+
+/*
+ * kda_conv_bwd -- gradients of kda_conv_fwd for dout = dLoss/dout and
+ * dfinal_state = dLoss/dfinal_state (NULL: zeros).
+ *   dx              [T, C] of x's type, written in full
+ *   dweight         fp32 [C, W]; dbias fp32 [C] or NULL (not written)
+ *   dinitial_state  [N, W - 1, C] of x's type, or NULL (not written)
+ */
+kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias,
+                          int32_t activation, const int32_t* cu_seqlens, int32_t num_seqs,
+                          const kda_tensor_t* initial_state, const kda_tensor_t* dout,
+                          const kda_tensor_t* dfinal_state, const kda_tensor_t* dx, const kda_tensor_t* dweight,
+                          const kda_tensor_t* dbias, const kda_tensor_t* dinitial_state, void* stream);
+
+/*
+ * kda_ssm_fwd -- the selective state space scan of a packed batch: a linear
+ * recurrence like KDA's with a diagonal state, S states per channel, whose
+ * steps and inputs depend on the token. Per channel c of group g = c / (C / G):
+ *
+ *   d_t = dt_t + dt_bias, or log(1 + exp(dt_t + dt_bias)) with dt_softplus != 0
+ *   h_t[n] = exp(d_t A[c, n]) h_{t-1}[n] + d_t u_t B_t[g, n]
+ *   y_t = sum_n C_t[g, n] h_t[n] + D u_t
+ *   out_t = y_t, or y_t z_t sigmoid(z_t) with a gate z
+ *
+ *   u, dt, z, out   [T, C]      z may be NULL; C <= 2^17
+ *   A               fp32 [C, S] decay rates, 1 <= S <= 128, usually negative
+ *                   (results are undefined where d A overflows)
+ *   B, C            [T, G, S]   C a multiple of G
+ *   D, dt_bias      fp32 [C] or NULL (zeros)
+ *   initial_state   fp32 [N, C, S] or NULL (zeros)
+ *   final_state     the same or NULL; may be initial_state itself
+ */
+kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                         const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,
+                         const kda_tensor_t* dt_bias, int32_t dt_softplus, const int32_t* cu_seqlens,
+                         int32_t num_seqs, const kda_tensor_t* initial_state, const kda_tensor_t* out,
+                         const kda_tensor_t* final_state, void* stream);
+
+/*
+ * kda_ssm_decode -- one token of each of B requests: token tensors [B, ...] as
+ * above, state fp32 [P, C, S] read and written in place, state_indices as for
+ * kda_decode.
+ */
+kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A,
+                            const kda_tensor_t* B, const kda_tensor_t* C, const kda_tensor_t* D,
+                            const kda_tensor_t* z, const kda_tensor_t* dt_bias, int32_t dt_softplus,
+                            const kda_tensor_t* state, const int32_t* state_indices, const kda_tensor_t* out,
+                            void* stream);
+
+/*
+ * kda_ssm_bwd -- gradients of kda_ssm_fwd for dout = dLoss/dout and
+ * dfinal_state = dLoss/dfinal_state (fp32 [N, C, S] or NULL: zeros).
+ *   du, ddt, dz     [T, C] of u's type; dz is NULL exactly when z is
+ *   dB, dC          [T, G, S] of u's type (sums over a group's channels)
+ *   dA              fp32 [C, S]; dD, ddt_bias fp32 [C] or NULL (not written)
+ *   dinitial_state  fp32 [N, C, S] or NULL (not written)
+ * All written in full. Scratch from the pool: a state every 16 tokens and the
+ * partial sums of dB and dC.
+ */
+kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                         const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,
+                         const kda_tensor_t* dt_bias, int32_t dt_softplus, const int32_t* cu_seqlens,
+                         int32_t num_seqs, const kda_tensor_t* initial_state, const kda_tensor_t* dout,
+                         const kda_tensor_t* dfinal_state, const kda_tensor_t* du, const kda_tensor_t* ddt,
+                         const kda_tensor_t* dA, const kda_tensor_t* dB, const kda_tensor_t* dC,
+                         const kda_tensor_t* dD, const kda_tensor_t* dz, const kda_tensor_t* ddt_bias,
+                         const kda_tensor_t* dinitial_state, void* stream);
+
 /* Human-readable text of a status code (static storage, never NULL). */
 const char* kda_status_string(kda_status_t status);
 
@@ -348,7 +471,8 @@ const char* kda_last_cuda_error(void);
  *                              partition of [0, T) (those results are wrong)
  *   KDA_DEVICE_WAIT_TIMEOUT    a bounded in-kernel wait ran out of budget (the
  *                              kernel stopped early; its results are undefined)
- *   KDA_DEVICE_BAD_STATE_INDEX kda_decode met a state index outside [0, P)
+ *   KDA_DEVICE_BAD_STATE_INDEX kda_decode, kda_conv_decode or kda_ssm_decode met
+ *                              a state index outside [0, P)
  *                              (that request was skipped)
  * Writes the bits to *flags (synchronising with the device), clears them when
  * `reset` is non-zero, and returns KDA_ERR_DEVICE if any bit is set, else

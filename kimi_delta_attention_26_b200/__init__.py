@@ -10,11 +10,13 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
 
-__all__ = ["kda_fwd", "kda_fwd_fused", "kda_decode", "kda_bwd", "library_path", "wait_timeouts", "device_status", "set_slice_columns", "set_path",
+__all__ = ["kda_fwd", "kda_fwd_fused", "kda_decode", "kda_bwd", "kda_conv_fwd", "kda_conv_decode", "kda_conv_bwd",
+           "kda_ssm_fwd", "kda_ssm_decode", "kda_ssm_bwd", "library_path", "wait_timeouts", "device_status", "set_slice_columns", "set_path",
            "set_time_split", "set_schedule", "describe", "KDAError", "HEAD_DIM"]
 
 HEAD_DIM = 128
@@ -28,8 +30,8 @@ if not os.path.exists(_LIB_PATH):
 
 _lib = ctypes.CDLL(_LIB_PATH)
 
-KDA_BF16, KDA_F32, KDA_I32 = 1, 2, 3
-_DTYPE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.int32: KDA_I32}
+KDA_BF16, KDA_F32, KDA_I32, KDA_F16 = 1, 2, 3, 4
+_DTYPE = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.int32: KDA_I32, torch.float16: KDA_F16}
 
 
 class TensorDesc(ctypes.Structure):
@@ -85,6 +87,16 @@ _lib.kda_bwd.argtypes = [_T, _T, _T, _T, _T, ctypes.c_float, _P, ctypes.c_int32,
 _lib.kda_bwd.restype = ctypes.c_int
 _lib.kda_decode.argtypes = [_T, _T, _T, _T, _T, ctypes.c_float, _T, _P, _T, _P]
 _lib.kda_decode.restype = ctypes.c_int
+# The convolution and the scan take their descriptors packed (bytes), see _pack.
+_I = ctypes.c_int32
+_lib.kda_conv_fwd.argtypes = [_P, _P, _P, _I, _P, _I, _P, _P, _P, _P]
+_lib.kda_conv_decode.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P]
+_lib.kda_conv_bwd.argtypes = [_P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, _P]
+_lib.kda_ssm_fwd.argtypes = [_P] * 8 + [_I, _P, _I] + [_P] * 4
+_lib.kda_ssm_decode.argtypes = [_P] * 8 + [_I] + [_P] * 4
+_lib.kda_ssm_bwd.argtypes = [_P] * 8 + [_I, _P, _I] + [_P] * 13
+for _f in ("kda_conv_fwd", "kda_conv_decode", "kda_conv_bwd", "kda_ssm_fwd", "kda_ssm_decode", "kda_ssm_bwd"):
+    getattr(_lib, _f).restype = ctypes.c_int
 
 
 class KDAError(RuntimeError):
@@ -328,3 +340,306 @@ def kda_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, 
     if rc != 0:
         raise KDAError(rc)
     return grads
+
+
+# ------------------------------------------------- short convolution and scan
+_ACTIVATION = {None: 0, "silu": 1}
+_DESC = struct.Struct("@Pii4q4q")
+_PAD = (0, 0, 0, 0)
+
+
+def _pack(t: Optional[torch.Tensor], name: str, index: int):
+    """``kda_tensor_t`` of a tensor on CUDA device `index`, as bytes (None -> NULL)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    n = t.dim()
+    if n > 4:
+        raise ValueError(f"{name} has more than 4 dimensions")
+    return _DESC.pack(t.data_ptr(), n, _DTYPE.get(t.dtype, 0), *t.shape, *_PAD[n:], *t.stride(), *_PAD[n:])
+
+
+def _device_of(t: torch.Tensor, name: str, dims: int, fn: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if not t.is_cuda:
+        raise ValueError(f"{fn} runs on CUDA tensors only")
+    return t.get_device()
+
+
+def _int32_ptr(t: Optional[torch.Tensor], name: str, index: int, n: Optional[int] = None):
+    """Address of a contiguous int32 vector (of n elements) on the device."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{name} must be a torch.int32 tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dim() != 1 or not t.is_contiguous() or (t.numel() < 2 if n is None else t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous vector" + ("" if n is None else f" of {n} elements"))
+    return t.data_ptr()
+
+
+class _On:
+    """The device and stream of a call: outputs are allocated for that stream,
+    and tensors of another stream are kept until its work is done."""
+
+    def __init__(self, index: int, stream: Optional[torch.cuda.Stream], tensors):
+        if stream.device_index != index:
+            raise ValueError(f"stream is on {stream.device}, expected cuda:{index}")
+        self.stream, self.tensors = stream, tensors
+
+    def __enter__(self):
+        self.context = torch.cuda.stream(self.stream)
+        self.context.__enter__()
+
+    def __exit__(self, *exc):
+        self.context.__exit__(*exc)
+        for t in self.tensors:
+            if t is not None and exc[0] is None:
+                t.record_stream(self.stream)
+
+
+class _Here:
+    """The current stream of the current device: nothing to switch."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return None
+
+
+_HERE = _Here()
+
+
+def _on(index: int, stream: Optional[torch.cuda.Stream], tensors):
+    if stream is not None:
+        return _On(index, stream, tensors)
+    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+def _raise(code: int, checks) -> None:
+    """The error of a refused call: what is wrong with a tensor, where the checks find it, else the status."""
+    for t, name, dtype, shape, contiguous in checks:
+        if t is not None:
+            _check(t, name, dtype, shape, t.device, contiguous)
+    raise KDAError(code)
+
+
+def _activation(name: Optional[str]) -> int:
+    if name not in _ACTIVATION:
+        raise ValueError(f"activation must be None or 'silu', got {name!r}")
+    return _ACTIVATION[name]
+
+
+def kda_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                 activation: Optional[str] = "silu", cu_seqlens: Optional[torch.Tensor] = None,
+                 initial_state: Optional[torch.Tensor] = None, output_final_state: bool = True,
+                 out: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None):
+    """Short causal depthwise convolution of packed sequences (see ``include/kda.h``).
+
+    x: [T, C] bf16, fp16 or fp32; weight: fp32 [C, W], W in 2..4; bias: fp32 [C]
+    or None; activation: "silu" or None; cu_seqlens: int32 [N + 1] on the device
+    (None: one sequence; tokens behind the last sequence are left as they were);
+    initial_state: [N, W - 1, C] of x's type (the inputs before each sequence,
+    oldest first) or None. Returns ``(out, final_state)``; ``final_state`` is
+    None unless requested.
+    """
+    dev = _device_of(x, "x", 2, "kda_conv_fwd")
+    act = _activation(activation)
+    cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
+    N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C, W]")
+    (T, C), W = x.shape, weight.shape[1]
+    with _on(dev, stream, (x, weight, bias, cu_seqlens, initial_state, out, final_state)):
+        if out is None:
+            out = torch.empty((T, C), dtype=x.dtype, device=x.device)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
+        rc = _lib.kda_conv_fwd(_pack(x, "x", dev), _pack(weight, "weight", dev), _pack(bias, "bias", dev), act, cu, N,
+                               _pack(initial_state, "initial_state", dev), _pack(out, "out", dev),
+                               _pack(final_state, "final_state", dev), torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        t = x.dtype
+        _raise(rc, [(weight, "weight", torch.float32, (C, W), True), (bias, "bias", torch.float32, (C,), True),
+                    (initial_state, "initial_state", t, (N, W - 1, C), True), (out, "out", t, (T, C), False),
+                    (final_state, "final_state", t, (N, W - 1, C), True)])
+    return out, final_state
+
+
+def kda_conv_decode(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    activation: Optional[str] = "silu", state_indices: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One token of the convolution for B requests (see ``include/kda.h``):
+    returns the outputs and moves each request's state on, in place.
+
+    x: [B, C]; state: [P, W - 1, C] of x's type; state_indices: int32 [B] on the
+    device (distinct slots), or None for slot b; out may be x.
+    """
+    dev = _device_of(x, "x", 2, "kda_conv_decode")
+    act = _activation(activation)
+    B, C = x.shape
+    idx = _int32_ptr(state_indices, "state_indices", dev, B)
+    with _on(dev, stream, (x, weight, bias, state, state_indices, out)):
+        if out is None:
+            out = torch.empty((B, C), dtype=x.dtype, device=x.device)
+        rc = _lib.kda_conv_decode(_pack(x, "x", dev), _pack(weight, "weight", dev), _pack(bias, "bias", dev), act,
+                                  _pack(state, "state", dev), idx, _pack(out, "out", dev),
+                                  torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        W = weight.shape[-1]
+        _raise(rc, [(weight, "weight", torch.float32, (C, W), True), (bias, "bias", torch.float32, (C,), True),
+                    (state, "state", x.dtype, (state.shape[0], W - 1, C), True), (out, "out", x.dtype, (B, C), False)])
+    return out
+
+
+def kda_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                 activation: Optional[str] = "silu", cu_seqlens: Optional[torch.Tensor] = None,
+                 initial_state: Optional[torch.Tensor] = None, dfinal_state: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of ``kda_conv_fwd`` (see ``include/kda.h``): a dict of ``dx``
+    [T, C] and ``dinitial_state`` [N, W - 1, C] of x's type, ``dweight`` fp32
+    [C, W] and ``dbias`` fp32 [C] (None without a bias), for the output's
+    gradient ``dout`` and the final state's (or None)."""
+    dev = _device_of(x, "x", 2, "kda_conv_bwd")
+    act = _activation(activation)
+    cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
+    N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C, W]")
+    (T, C), W = x.shape, weight.shape[1]
+    with _on(dev, stream, (x, weight, bias, cu_seqlens, initial_state, dout, dfinal_state)):
+        dx = torch.empty((T, C), dtype=x.dtype, device=x.device)
+        dw = torch.empty((C, W), dtype=torch.float32, device=x.device)
+        db = None if bias is None else torch.empty((C,), dtype=torch.float32, device=x.device)
+        di = torch.empty((N, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
+        rc = _lib.kda_conv_bwd(_pack(x, "x", dev), _pack(weight, "weight", dev), _pack(bias, "bias", dev), act, cu, N,
+                               _pack(initial_state, "initial_state", dev), _pack(dout, "dout", dev),
+                               _pack(dfinal_state, "dfinal_state", dev), _pack(dx, "dx", dev),
+                               _pack(dw, "dweight", dev), _pack(db, "dbias", dev), _pack(di, "dinitial_state", dev),
+                               torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        t = x.dtype
+        _raise(rc, [(weight, "weight", torch.float32, (C, W), True), (bias, "bias", torch.float32, (C,), True),
+                    (initial_state, "initial_state", t, (N, W - 1, C), True), (dout, "dout", t, (T, C), False),
+                    (dfinal_state, "dfinal_state", t, (N, W - 1, C), True)])
+    return {"dx": dx, "dweight": dw, "dbias": db, "dinitial_state": di}
+
+
+def _ssm_checks(u, dt, A, B, C, D, z, dt_bias):
+    t, (T, c) = u.dtype, u.shape
+    n, g = A.shape[-1], B.shape[1] if B.dim() == 3 else 1
+    return [(dt, "dt", t, (T, c), False), (A, "A", torch.float32, (c, n), True), (B, "B", t, (T, g, n), False),
+            (C, "C", t, (T, g, n), False), (D, "D", torch.float32, (c,), True), (z, "z", t, (T, c), False),
+            (dt_bias, "dt_bias", torch.float32, (c,), True)]
+
+
+def kda_ssm_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                cu_seqlens: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                output_final_state: bool = True, out: Optional[torch.Tensor] = None,
+                final_state: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Selective state space scan of packed sequences (see ``include/kda.h``).
+
+    u, dt: [T, C] bf16, fp16 or fp32; A: fp32 [C, S]; B, C: [T, G, S] of u's
+    type; D, dt_bias: fp32 [C] or None; z: the gate, [T, C] of u's type, or None;
+    dt_softplus: whether the step is log(1 + exp(dt + dt_bias)); cu_seqlens:
+    int32 [N + 1] on the device (None: one sequence; tokens behind the last
+    sequence are left as they were); initial_state: fp32 [N, C, S] or None.
+    Returns ``(out, final_state)``; ``final_state`` is None unless requested and
+    may be the initial state's tensor.
+    """
+    dev = _device_of(u, "u", 2, "kda_ssm_fwd")
+    cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
+    N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    T, c = u.shape
+    with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, out, final_state)):
+        if out is None:
+            out = torch.empty((T, c), dtype=u.dtype, device=u.device)
+        if final_state is None and output_final_state:
+            final_state = torch.empty((N, c, A.shape[-1]), dtype=torch.float32, device=u.device)
+        rc = _lib.kda_ssm_fwd(_pack(u, "u", dev), _pack(dt, "dt", dev), _pack(A, "A", dev), _pack(B, "B", dev),
+                              _pack(C, "C", dev), _pack(D, "D", dev), _pack(z, "z", dev),
+                              _pack(dt_bias, "dt_bias", dev), bool(dt_softplus), cu, N,
+                              _pack(initial_state, "initial_state", dev), _pack(out, "out", dev),
+                              _pack(final_state, "final_state", dev), torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        state = (N, c, A.shape[-1])
+        _raise(rc, _ssm_checks(u, dt, A, B, C, D, z, dt_bias) +
+               [(initial_state, "initial_state", torch.float32, state, True), (out, "out", u.dtype, (T, c), False),
+                (final_state, "final_state", torch.float32, state, True)])
+    return out, final_state
+
+
+def kda_ssm_decode(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                   state: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                   dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                   state_indices: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """One token of the scan for R requests (see ``include/kda.h``): returns the
+    outputs and moves each request's state on, in place.
+
+    u, dt, z: [R, C]; B, C: [R, G, S]; state: fp32 [P, C, S]; state_indices:
+    int32 [R] on the device (distinct slots), or None for slot r.
+    """
+    dev = _device_of(u, "u", 2, "kda_ssm_decode")
+    R, c = u.shape
+    idx = _int32_ptr(state_indices, "state_indices", dev, R)
+    with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, state, state_indices, out)):
+        if out is None:
+            out = torch.empty((R, c), dtype=u.dtype, device=u.device)
+        rc = _lib.kda_ssm_decode(_pack(u, "u", dev), _pack(dt, "dt", dev), _pack(A, "A", dev), _pack(B, "B", dev),
+                                 _pack(C, "C", dev), _pack(D, "D", dev), _pack(z, "z", dev),
+                                 _pack(dt_bias, "dt_bias", dev), bool(dt_softplus), _pack(state, "state", dev), idx,
+                                 _pack(out, "out", dev), torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        _raise(rc, _ssm_checks(u, dt, A, B, C, D, z, dt_bias) +
+               [(state, "state", torch.float32, (state.shape[0], c, A.shape[-1]), True),
+                (out, "out", u.dtype, (R, c), False)])
+    return out
+
+
+def kda_ssm_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                dout: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
+                cu_seqlens: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                dfinal_state: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of ``kda_ssm_fwd`` (see ``include/kda.h``) for the output's
+    gradient ``dout`` and the final state's (or None): a dict of ``du``, ``ddt``,
+    ``dz`` [T, C], ``dB``, ``dC`` [T, G, S] of u's type and fp32 ``dA`` [C, S],
+    ``dD``, ``ddt_bias`` [C], ``dinitial_state`` [N, C, S]; None for ``dz``,
+    ``dD`` and ``ddt_bias`` whose input is None."""
+    dev = _device_of(u, "u", 2, "kda_ssm_bwd")
+    cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
+    N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    (T, c), f32 = u.shape, torch.float32
+    if A.dim() != 2 or B.dim() != 3:
+        raise ValueError("A must be [C, S] and B [T, G, S]")
+    with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, dout, dfinal_state)):
+        def new(shape, dtype=u.dtype, of=u):
+            return None if of is None else torch.empty(shape, dtype=dtype, device=u.device)
+
+        gr = {"du": new((T, c)), "ddt": new((T, c)), "dA": new(A.shape, f32), "dB": new(B.shape), "dC": new(B.shape),
+              "dD": new((c,), f32, D), "dz": new((T, c), u.dtype, z), "ddt_bias": new((c,), f32, dt_bias),
+              "dinitial_state": new((N, c, A.shape[1]), f32)}
+        rc = _lib.kda_ssm_bwd(_pack(u, "u", dev), _pack(dt, "dt", dev), _pack(A, "A", dev), _pack(B, "B", dev),
+                              _pack(C, "C", dev), _pack(D, "D", dev), _pack(z, "z", dev),
+                              _pack(dt_bias, "dt_bias", dev), bool(dt_softplus), cu, N,
+                              _pack(initial_state, "initial_state", dev), _pack(dout, "dout", dev),
+                              _pack(dfinal_state, "dfinal_state", dev), *(_pack(t, n, dev) for n, t in gr.items()),
+                              torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        state = (N, c, A.shape[1])
+        _raise(rc, _ssm_checks(u, dt, A, B, C, D, z, dt_bias) +
+               [(initial_state, "initial_state", f32, state, True), (dout, "dout", u.dtype, (T, c), False),
+                (dfinal_state, "dfinal_state", f32, state, True)])
+    return gr

@@ -11,7 +11,8 @@ ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", "kda_api.cu")]
 HEADERS = [os.path.join(ROOT, "include", "kda.h"), os.path.abspath(__file__)] + [
     os.path.join(PKG, "csrc", f) for f in ("kda_prims.cuh", "kda_fwd16.cuh", "kda_fwd64.cuh", "kda_split.cuh", "kda_decode.cuh",
-                                            "kda_bwd.cuh")]
+                                            "kda_bwd.cuh", "kda_io.cuh", "kda_conv.cuh", "kda_conv_api.cuh",
+                                            "kda_ssm.cuh", "kda_ssm_api.cuh")]
 LIB = os.path.join(PKG, "libkda.so")
 
 NVCC_FLAGS = [

@@ -13,12 +13,16 @@
 #include "kda_split.cuh"
 #include "kda_decode.cuh"
 #include "kda_bwd.cuh"
+#include "kda_conv.cuh"
+#include "kda_ssm.cuh"
 
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
+#include <type_traits>
 
 namespace {
 
@@ -622,6 +626,10 @@ kda_status_t fwd_pooled(const Problem& P, void* stream) {
 
 }  // namespace
 
+// the entry points of the short convolution and of the selective scan
+#include "kda_conv_api.cuh"
+#include "kda_ssm_api.cuh"
+
 extern "C" {
 
 kda_status_t kda_fwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* v, const kda_tensor_t* g,
@@ -838,6 +846,7 @@ const char* kda_status_string(kda_status_t s) {
     case KDA_ERR_STRIDE: return "a tensor's strides are not supported";
     case KDA_ERR_DEVICE: return "the device recorded a fault (see kda_device_status)";
     case KDA_ERR_VALUE: return "a scalar argument is out of its range";
+    case KDA_ERR_OVERLAP: return "an output overlaps an input or another output";
   }
   return "unknown status";
 }

@@ -1,0 +1,310 @@
+// kda_ssm_api.cuh -- argument checks and launches of the scan's entry points.
+// Part of kda_api.cu's translation unit, after kda_conv_api.cuh.
+#pragma once
+
+namespace {
+
+constexpr int64_t kSsmMaxChannels = 1 << 17;
+constexpr int64_t kSsmMaxStates = 128;
+
+struct SsmArgs {
+  int64_t T, C, N, G;
+  kda_dtype_t dt;
+  RowView u, dt_, b, c, z, out;  // out: dout for the backward pass
+  void *A, *D, *bias;
+  Span s_A, s_D, s_bias;
+};
+
+kda_status_t check_ssm(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                       const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z, const kda_tensor_t* dt_bias,
+                       const kda_tensor_t* out, bool written, SsmArgs* a) {
+  if (!u || !dt || !A || !B || !C || !out) return KDA_ERR_NULL;
+  if (!io_bytes(u->dtype)) return KDA_ERR_DTYPE;
+  if (u->ndim != 2 || A->ndim != 2 || B->ndim != 3) return KDA_ERR_SHAPE;
+  a->dt = u->dtype;
+  a->T = u->shape[0];
+  a->C = u->shape[1];
+  a->N = A->shape[1];
+  a->G = B->shape[1];
+  if (a->T < 0 || a->T > kMaxRows || a->C < 1 || a->C > kSsmMaxChannels || a->N < 1 || a->N > kSsmMaxStates ||
+      a->G < 1 || a->G > a->C || a->C % a->G != 0)
+    return KDA_ERR_SHAPE;
+  kda_status_t st;
+  if ((st = view_rows(u, a->dt, a->T, 0, a->C, false, &a->u)) != KDA_OK ||
+      (st = view_rows(dt, a->dt, a->T, 0, a->C, false, &a->dt_)) != KDA_OK ||
+      (st = view_packed(A, KDA_F32, {a->C, a->N}, false, &a->A, &a->s_A)) != KDA_OK ||
+      (st = view_rows(B, a->dt, a->T, a->G, a->N, false, &a->b)) != KDA_OK ||
+      (st = view_rows(C, a->dt, a->T, a->G, a->N, false, &a->c)) != KDA_OK ||
+      (st = view_packed(D, KDA_F32, {a->C}, true, &a->D, &a->s_D)) != KDA_OK ||
+      (z && (st = view_rows(z, a->dt, a->T, 0, a->C, false, &a->z)) != KDA_OK) ||
+      (st = view_packed(dt_bias, KDA_F32, {a->C}, true, &a->bias, &a->s_bias)) != KDA_OK ||
+      (st = view_rows(out, a->dt, a->T, 0, a->C, written, &a->out)) != KDA_OK)
+    return st;
+  return KDA_OK;
+}
+
+// Threads per channel: each holds ssm::S of its states.
+template <typename F>
+void by_lanes(int64_t N, F f) {
+  const int64_t l = (N + kda::ssm::S - 1) / kda::ssm::S;
+  if (l <= 4) f(std::integral_constant<int, 4>());
+  else if (l <= 8) f(std::integral_constant<int, 8>());
+  else if (l <= 16) f(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 32>());
+}
+
+template <typename F>
+void by_ssm(kda_dtype_t dt, int64_t N, F f) {
+  by_lanes(N, [&](auto l) {
+    if (dt == KDA_BF16) f(__nv_bfloat16(), l);
+    else if (dt == KDA_F16) f(__half(), l);
+    else f(float(), l);
+  });
+}
+
+kda::ssm::Params ssm_params(const SsmArgs& a, int32_t softplus, const int32_t* cu, int32_t num_seqs, const void* init) {
+  kda::ssm::Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.u = a.u.data;
+  p.dt = a.dt_.data;
+  p.z = a.z.data;
+  p.b = a.b.data;
+  p.c = a.c.data;
+  p.A = static_cast<const float*>(a.A);
+  p.D = static_cast<const float*>(a.D);
+  p.dt_bias = static_cast<const float*>(a.bias);
+  p.cu = cu;
+  p.init = static_cast<const float*>(init);
+  p.T = a.T;
+  p.u_st = a.u.st;
+  p.dt_st = a.dt_.st;
+  p.z_st = a.z.st;
+  p.b_st = a.b.st;
+  p.b_sg = a.b.sg;
+  p.c_st = a.c.st;
+  p.c_sg = a.c.sg;
+  p.NS = num_seqs;
+  p.C = static_cast<int>(a.C);
+  p.N = static_cast<int>(a.N);
+  p.G = static_cast<int>(a.G);
+  p.softplus = softplus;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                         const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,
+                         const kda_tensor_t* dt_bias, int32_t dt_softplus, const int32_t* cu_seqlens, int32_t num_seqs,
+                         const kda_tensor_t* initial_state, const kda_tensor_t* out, const kda_tensor_t* final_state,
+                         void* stream) {
+  namespace sm = kda::ssm;
+  g_last_cuda_error[0] = '\0';
+  SsmArgs a;
+  kda_status_t st = check_ssm(u, dt, A, B, C, D, z, dt_bias, out, true, &a);
+  if (st != KDA_OK) return st;
+  if ((st = check_packing_args(cu_seqlens, num_seqs, a.T)) != KDA_OK) return st;
+  void *init, *fin;
+  Span s_init, s_fin;
+  if ((st = view_packed(initial_state, KDA_F32, {num_seqs, a.C, a.N}, true, &init, &s_init)) != KDA_OK ||
+      (st = view_packed(final_state, KDA_F32, {num_seqs, a.C, a.N}, true, &fin, &s_fin)) != KDA_OK)
+    return st;
+  // a block reads its part of the initial state before it writes that of the final one: they may be the same tensor
+  if (any_overlap({a.out.span, s_fin},
+                  {a.u.span, a.dt_.span, a.b.span, a.c.span, a.z.span, a.s_A, a.s_D, a.s_bias}) ||
+      overlap(a.out.span, s_init) || (init != fin && overlap(s_fin, s_init)))
+    return KDA_ERR_OVERLAP;
+  int dev = 0;
+  if ((st = prologue(&dev)) != KDA_OK) return st;
+  sm::Params p = ssm_params(a, dt_softplus != 0, cu_seqlens, num_seqs, init);
+  p.out = a.out.data;
+  p.o_st = a.out.st;
+  p.fin = static_cast<float*>(fin);
+  by_ssm(a.dt, a.N, [&](auto t, auto l) {
+    constexpr int CH = sm::NTHREADS / l.value;
+    p.blocks_per_group = static_cast<int>((a.C / a.G + CH - 1) / CH);
+    sm::ssm_fwd_kernel<decltype(t), l.value, true>
+        <<<dim3(static_cast<unsigned>(a.G * p.blocks_per_group), num_seqs), sm::NTHREADS, 0,
+           static_cast<cudaStream_t>(stream)>>>(p);
+  });
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
+}
+
+kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                            const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,
+                            const kda_tensor_t* dt_bias, int32_t dt_softplus, const kda_tensor_t* state,
+                            const int32_t* state_indices, const kda_tensor_t* out, void* stream) {
+  namespace sm = kda::ssm;
+  g_last_cuda_error[0] = '\0';
+  SsmArgs a;
+  kda_status_t st = check_ssm(u, dt, A, B, C, D, z, dt_bias, out, true, &a);
+  if (st != KDA_OK) return st;
+  if (!state) return KDA_ERR_NULL;
+  if (state->ndim != 3) return KDA_ERR_SHAPE;
+  const int64_t B_ = a.T, pool = state->shape[0];
+  if (pool < 1 || (!state_indices && pool < B_) || pool > (int64_t(1) << 40) / (a.C * a.N)) return KDA_ERR_SHAPE;
+  void* sp;
+  Span s_state;
+  if ((st = view_packed(state, KDA_F32, {pool, a.C, a.N}, false, &sp, &s_state)) != KDA_OK) return st;
+  if (reinterpret_cast<uintptr_t>(state_indices) & 3u) return KDA_ERR_ALIGN;
+  if (any_overlap({a.out.span, s_state},
+                  {a.u.span, a.dt_.span, a.b.span, a.c.span, a.z.span, a.s_A, a.s_D, a.s_bias}))
+    return KDA_ERR_OVERLAP;
+  int dev = 0;
+  if ((st = prologue(&dev)) != KDA_OK) return st;
+  if (B_ == 0) return KDA_OK;
+  sm::DecodeParams p;
+  p.u = a.u.data;
+  p.dt = a.dt_.data;
+  p.z = a.z.data;
+  p.b = a.b.data;
+  p.c = a.c.data;
+  p.A = static_cast<const float*>(a.A);
+  p.D = static_cast<const float*>(a.D);
+  p.dt_bias = static_cast<const float*>(a.bias);
+  p.state = static_cast<float*>(sp);
+  p.idx = state_indices;
+  p.out = a.out.data;
+  p.pool = pool;
+  p.u_st = a.u.st;
+  p.dt_st = a.dt_.st;
+  p.z_st = a.z.st;
+  p.o_st = a.out.st;
+  p.b_st = a.b.st;
+  p.b_sg = a.b.sg;
+  p.c_st = a.c.st;
+  p.c_sg = a.c.sg;
+  p.C = static_cast<int>(a.C);
+  p.N = static_cast<int>(a.N);
+  p.G = static_cast<int>(a.G);
+  p.softplus = dt_softplus != 0;
+  by_ssm(a.dt, a.N, [&](auto t, auto l) {
+    constexpr int CH = sm::NTHREADS / l.value;
+    sm::ssm_decode_kernel<decltype(t), l.value>
+        <<<dim3(static_cast<unsigned>(B_), static_cast<unsigned>((a.C + CH - 1) / CH)), sm::NTHREADS, 0,
+           static_cast<cudaStream_t>(stream)>>>(p);
+  });
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
+}
+
+kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
+                         const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,
+                         const kda_tensor_t* dt_bias, int32_t dt_softplus, const int32_t* cu_seqlens, int32_t num_seqs,
+                         const kda_tensor_t* initial_state, const kda_tensor_t* dout, const kda_tensor_t* dfinal_state,
+                         const kda_tensor_t* du, const kda_tensor_t* ddt, const kda_tensor_t* dA,
+                         const kda_tensor_t* dB, const kda_tensor_t* dC, const kda_tensor_t* dD, const kda_tensor_t* dz,
+                         const kda_tensor_t* ddt_bias, const kda_tensor_t* dinitial_state, void* stream) {
+  namespace sm = kda::ssm;
+  g_last_cuda_error[0] = '\0';
+  SsmArgs a;
+  kda_status_t st = check_ssm(u, dt, A, B, C, D, z, dt_bias, dout, false, &a);
+  if (st != KDA_OK) return st;
+  if ((st = check_packing_args(cu_seqlens, num_seqs, a.T)) != KDA_OK) return st;
+  if ((z != nullptr) != (dz != nullptr)) return KDA_ERR_NULL;  // the gate and its gradient come together
+  void *init, *dfin, *dinit, *da, *dd, *dbias;
+  Span s_init, s_dfin, s_dinit, s_da, s_dd, s_dbias;
+  RowView vdu, vddt, vdz, vdb, vdc;
+  if ((st = view_packed(initial_state, KDA_F32, {num_seqs, a.C, a.N}, true, &init, &s_init)) != KDA_OK ||
+      (st = view_packed(dfinal_state, KDA_F32, {num_seqs, a.C, a.N}, true, &dfin, &s_dfin)) != KDA_OK ||
+      (st = view_rows(du, a.dt, a.T, 0, a.C, true, &vdu)) != KDA_OK ||
+      (st = view_rows(ddt, a.dt, a.T, 0, a.C, true, &vddt)) != KDA_OK ||
+      (st = view_packed(dA, KDA_F32, {a.C, a.N}, false, &da, &s_da)) != KDA_OK ||
+      (st = view_rows(dB, a.dt, a.T, a.G, a.N, true, &vdb)) != KDA_OK ||
+      (st = view_rows(dC, a.dt, a.T, a.G, a.N, true, &vdc)) != KDA_OK ||
+      (st = view_packed(dD, KDA_F32, {a.C}, true, &dd, &s_dd)) != KDA_OK ||
+      (dz && (st = view_rows(dz, a.dt, a.T, 0, a.C, true, &vdz)) != KDA_OK) ||
+      (st = view_packed(ddt_bias, KDA_F32, {a.C}, true, &dbias, &s_dbias)) != KDA_OK ||
+      (st = view_packed(dinitial_state, KDA_F32, {num_seqs, a.C, a.N}, true, &dinit, &s_dinit)) != KDA_OK)
+    return st;
+  if (any_overlap({vdu.span, vddt.span, s_da, vdb.span, vdc.span, s_dd, vdz.span, s_dbias, s_dinit},
+                  {a.u.span, a.dt_.span, a.b.span, a.c.span, a.z.span, a.out.span, a.s_A, a.s_D, a.s_bias, s_init,
+                   s_dfin}))
+    return KDA_ERR_OVERLAP;
+  int dev = 0;
+  if ((st = prologue(&dev)) != KDA_OK) return st;
+  if ((st = prepare_pool(dev)) != KDA_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  sm::BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.f = ssm_params(a, dt_softplus != 0, cu_seqlens, num_seqs, init);
+  int blocks = 0;
+  by_ssm(a.dt, a.N, [&](auto, auto l) {
+    constexpr int CH = sm::NTHREADS / l.value;
+    p.f.blocks_per_group = static_cast<int>((a.C / a.G + CH - 1) / CH);
+    blocks = static_cast<int>(a.G) * p.f.blocks_per_group;
+  });
+  const size_t cn = static_cast<size_t>(a.C) * a.N;
+  const size_t ck_bytes = round256((static_cast<size_t>(a.T) / sm::TT + num_seqs) * cn * 4);
+  const size_t a_bytes = round256(num_seqs * cn * 4), d_bytes = round256(2 * static_cast<size_t>(num_seqs) * a.C * 4);
+  const size_t b_bytes = round256(static_cast<size_t>(blocks) * a.T * a.N * 4);
+  void* scratch = nullptr;
+  cudaError_t e = cudaMallocFromPoolAsync(&scratch, ck_bytes + a_bytes + d_bytes + 2 * b_bytes, g_pool[dev].load(), cs);
+  if (e != cudaSuccess) return cuda_fail(e);
+  unsigned char* sb = static_cast<unsigned char*>(scratch);
+  p.f.ck = reinterpret_cast<float*>(sb);
+  p.part_a = reinterpret_cast<float*>(sb + ck_bytes);
+  p.part_d = reinterpret_cast<float*>(sb + ck_bytes + a_bytes);
+  p.part_b = reinterpret_cast<float*>(sb + ck_bytes + a_bytes + d_bytes);
+  p.part_c = reinterpret_cast<float*>(sb + ck_bytes + a_bytes + d_bytes + b_bytes);
+  p.dout = a.out.data;
+  p.dout_st = a.out.st;
+  p.dfin = static_cast<const float*>(dfin);
+  p.du = vdu.data;
+  p.ddt = vddt.data;
+  p.dz = vdz.data;
+  p.du_st = vdu.st;
+  p.ddt_st = vddt.st;
+  p.dz_st = vdz.st;
+  p.dinit = static_cast<float*>(dinit);
+  sm::ReduceParams r;
+  std::memset(&r, 0, sizeof(r));
+  r.part_a = p.part_a;
+  r.part_d = p.part_d;
+  r.part_b = p.part_b;
+  r.part_c = p.part_c;
+  r.cu = cu_seqlens;
+  r.dA = static_cast<float*>(da);
+  r.dD = static_cast<float*>(dd);
+  r.ddt_bias = static_cast<float*>(dbias);
+  r.dB = vdb.data;
+  r.dC = vdc.data;
+  r.du = vdu.data;
+  r.ddt = vddt.data;
+  r.dz = vdz.data;
+  r.T = a.T;
+  r.dB_st = vdb.st;
+  r.dB_sg = vdb.sg;
+  r.dC_st = vdc.st;
+  r.dC_sg = vdc.sg;
+  r.du_st = vdu.st;
+  r.ddt_st = vddt.st;
+  r.dz_st = vdz.st;
+  r.NS = num_seqs;
+  r.C = static_cast<int>(a.C);
+  r.N = static_cast<int>(a.N);
+  r.G = static_cast<int>(a.G);
+  r.blocks_per_group = p.f.blocks_per_group;
+  const int64_t most = std::max<int64_t>(a.T * a.G * a.N, static_cast<int64_t>(cn));
+  const unsigned reduce_blocks =
+      static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 8 * static_cast<int64_t>(g_num_sms[dev])));
+  by_ssm(a.dt, a.N, [&](auto t, auto l) {
+    const dim3 grid(blocks, num_seqs);
+    sm::ssm_fwd_kernel<decltype(t), l.value, false><<<grid, sm::NTHREADS, 0, cs>>>(p.f);
+    constexpr size_t bytes = sizeof(sm::BwdShared<l.value>);
+    if (bytes > 48 * 1024)
+      cudaFuncSetAttribute(sm::ssm_bwd_kernel<decltype(t), l.value>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+    sm::ssm_bwd_kernel<decltype(t), l.value><<<grid, sm::NTHREADS, bytes, cs>>>(p);
+  });
+  by_ssm(a.dt, 1, [&](auto t, auto) { sm::ssm_reduce_kernel<decltype(t)><<<reduce_blocks, 256, 0, cs>>>(r); });
+  e = cudaGetLastError();
+  const cudaError_t ef = cudaFreeAsync(scratch, cs);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return ef != cudaSuccess ? cuda_fail(ef) : KDA_OK;
+}
+
+}  // extern "C"
