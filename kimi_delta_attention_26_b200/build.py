@@ -5,14 +5,16 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", "kda_api.cu")]
+CSRC = os.path.join(PKG, "csrc")
+SOURCES = [os.path.join(CSRC, f) for f in ("kda_api.cu", "kda_mixer_bf16.cu", "kda_mixer_f16.cu", "kda_mixer_f32.cu")]
 HEADERS = [os.path.join(ROOT, "include", "kda.h"), os.path.abspath(__file__)] + [
-    os.path.join(PKG, "csrc", f) for f in ("kda_prims.cuh", "kda_fwd16.cuh", "kda_fwd64.cuh", "kda_split.cuh", "kda_decode.cuh",
-                                            "kda_bwd.cuh", "kda_io.cuh", "kda_conv.cuh", "kda_conv_api.cuh",
-                                            "kda_ssm.cuh", "kda_ssm_api.cuh")]
+    os.path.join(CSRC, f) for f in ("kda_prims.cuh", "kda_fwd16.cuh", "kda_fwd64.cuh", "kda_split.cuh",
+                                    "kda_decode.cuh", "kda_bwd.cuh", "kda_io.cuh", "kda_conv.cuh", "kda_ssm.cuh",
+                                    "kda_mixer.cuh", "kda_mixer_impl.cuh", "kda_conv_api.cuh", "kda_ssm_api.cuh")]
 LIB = os.path.join(PKG, "libkda.so")
 
 NVCC_FLAGS = [
@@ -21,7 +23,7 @@ NVCC_FLAGS = [
     # Flush fp32 denormals: the gate exponentials run ~2.5x faster, and values
     # below 1.2e-38 are far under the bf16 resolution of every operand.
     "-ftz=true",
-    "-shared", "-Xcompiler", "-fPIC",
+    "-Xcompiler", "-fPIC",
     "-I", os.path.join(ROOT, "include"),
 ]
 
@@ -42,12 +44,22 @@ def stale() -> bool:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or stale():
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [nvcc(), *NVCC_FLAGS, "-o", tmp, *SOURCES]
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        subprocess.check_call(cmd)
-        os.replace(tmp, LIB)
+        # the translation units side by side, then one link
+        with tempfile.TemporaryDirectory(prefix="kda_build_") as tmp:
+            objects, running = [], []
+            for src in SOURCES:
+                obj = os.path.join(tmp, os.path.basename(src) + ".o")
+                cmd = [nvcc(), *NVCC_FLAGS, "-c", "-o", obj, src]
+                if verbose:
+                    print(" ".join(cmd), file=sys.stderr)
+                objects.append(obj)
+                running.append((cmd, subprocess.Popen(cmd)))
+            failed = [(cmd, p.returncode) for cmd, p in running if p.wait() != 0]
+            if failed:
+                raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+            lib = LIB + f".tmp{os.getpid()}"
+            subprocess.check_call([nvcc(), *NVCC_FLAGS, "-shared", "-o", lib, *objects])
+            os.replace(lib, LIB)
     return LIB
 
 

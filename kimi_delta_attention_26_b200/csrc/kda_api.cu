@@ -5,7 +5,9 @@
 //   kda_fwd64.cuh  64-token chunks on tcgen05
 // and, for one long sequence with few heads, the time-split prefill (the
 // 16-token kernel on both halves at once, combined by kda_split.cuh).
-// This file is the library's only translation unit.
+// The convolution's and the scan's entry points are in kda_conv_api.cuh and
+// kda_ssm_api.cuh, included here; their kernels are translation units of their
+// own (kda_mixer.cuh).
 
 #include "kda_prims.cuh"
 #include "kda_fwd16.cuh"
@@ -13,8 +15,7 @@
 #include "kda_split.cuh"
 #include "kda_decode.cuh"
 #include "kda_bwd.cuh"
-#include "kda_conv.cuh"
-#include "kda_ssm.cuh"
+#include "kda_mixer.cuh"
 
 #include <algorithm>
 #include <atomic>
@@ -630,6 +631,24 @@ kda_status_t fwd_pooled(const Problem& P, void* stream) {
 #include "kda_conv_api.cuh"
 #include "kda_ssm_api.cuh"
 
+namespace {
+
+// The status words of all translation units, OR-ed and added up, then cleared
+// where asked.
+cudaError_t status_words(uint32_t* flags, uint32_t* waits, bool reset_flags, bool reset_waits) {
+  cudaError_t e = cudaMemcpyFromSymbol(flags, kda::g_device_flags, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(waits, kda::g_wait_timeouts, sizeof(uint32_t));
+  const uint32_t zero = 0;
+  if (e == cudaSuccess && reset_flags) e = cudaMemcpyToSymbol(kda::g_device_flags, &zero, sizeof(uint32_t));
+  if (e == cudaSuccess && reset_waits) e = cudaMemcpyToSymbol(kda::g_wait_timeouts, &zero, sizeof(uint32_t));
+  if (e == cudaSuccess) e = kda::Mixer<__nv_bfloat16>::status(flags, waits, reset_flags, reset_waits);
+  if (e == cudaSuccess) e = kda::Mixer<__half>::status(flags, waits, reset_flags, reset_waits);
+  if (e == cudaSuccess) e = kda::Mixer<float>::status(flags, waits, reset_flags, reset_waits);
+  return e;
+}
+
+}  // namespace
+
 extern "C" {
 
 kda_status_t kda_fwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_tensor_t* v, const kda_tensor_t* g,
@@ -857,30 +876,20 @@ kda_status_t kda_device_status(uint32_t* flags, int32_t reset) {
   if (!flags) return KDA_ERR_NULL;
   g_last_cuda_error[0] = '\0';
   uint32_t bits = 0, waits = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&bits, kda::g_device_flags, sizeof(uint32_t));
-  if (e != cudaSuccess) return cuda_fail(e);
-  e = cudaMemcpyFromSymbol(&waits, kda::g_wait_timeouts, sizeof(uint32_t));
+  cudaError_t e = status_words(&bits, &waits, reset != 0, reset != 0);
   if (e != cudaSuccess) return cuda_fail(e);
   if (waits) bits |= KDA_DEVICE_WAIT_TIMEOUT;
   *flags = bits;
-  if (reset) {
-    const uint32_t zero = 0;
-    if ((e = cudaMemcpyToSymbol(kda::g_device_flags, &zero, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e);
-    if ((e = cudaMemcpyToSymbol(kda::g_wait_timeouts, &zero, sizeof(uint32_t))) != cudaSuccess) return cuda_fail(e);
-  }
   return bits ? KDA_ERR_DEVICE : KDA_OK;
 }
 
 kda_status_t kda_wait_timeouts(uint32_t* count, int32_t reset) {
   if (!count) return KDA_ERR_NULL;
   g_last_cuda_error[0] = '\0';
-  cudaError_t e = cudaMemcpyFromSymbol(count, kda::g_wait_timeouts, sizeof(uint32_t));
+  uint32_t bits = 0, waits = 0;
+  cudaError_t e = status_words(&bits, &waits, false, reset != 0);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (reset) {
-    const uint32_t zero = 0;
-    e = cudaMemcpyToSymbol(kda::g_wait_timeouts, &zero, sizeof(uint32_t));
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
+  *count = waits;
   return KDA_OK;
 }
 

@@ -104,17 +104,17 @@ __global__ void __launch_bounds__(NTHREADS) conv_fwd_kernel(Params p) {
     for (int i = 0; i < W - 1; ++i)
       load_position<T, V, W>(win[i], x, p.x_st, init, p.C, c, s, start, lo - (W - 1) + i);
     for (int64_t t = lo; t < hi; t += KT) {
-      Pack<T, V> raw[KT];
+      Vec<T, V> raw[KT];
 #pragma unroll
       for (int k = 0; k < KT; ++k)
-        if (t + k < hi) raw[k] = *reinterpret_cast<const Pack<T, V>*>(x + (t + k) * p.x_st + c);
+        if (t + k < hi) raw[k].load(x + (t + k) * p.x_st + c);
 #pragma unroll
       for (int k = 0; k < KT; ++k) {
         if (t + k >= hi) break;
         float y[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          win[W - 1 + k][i] = to_f32(raw[k].v[i]);
+          win[W - 1 + k][i] = raw[k].get(i);
           float a = b[i];
 #pragma unroll
           for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[k + j][i], a);
@@ -158,21 +158,21 @@ __global__ void __launch_bounds__(NTHREADS) conv_decode_kernel(DecodeParams p) {
   }
   if (c >= p.C) return;
   T* st = static_cast<T*>(p.state) + slot * (W - 1) * p.C + c;
-  Pack<T, V> raw[W];
+  Vec<T, V> raw[W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) raw[j] = *reinterpret_cast<const Pack<T, V>*>(st + j * p.C);
-  raw[W - 1] = *reinterpret_cast<const Pack<T, V>*>(static_cast<const T*>(p.x) + b * p.x_st + c);
+  for (int j = 0; j < W - 1; ++j) raw[j].load(st + j * p.C);
+  raw[W - 1].load(static_cast<const T*>(p.x) + b * p.x_st + c);
   float w[W][V], y[V];
   load_weights<V, W>(w, y, p.weight, p.bias, c);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], to_f32(raw[j].v[i]), y[i]);
+    for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], raw[j].get(i), y[i]);
     if (p.silu) y[i] = silu(y[i]);
   }
   store_f32<T, V>(static_cast<T*>(p.out) + b * p.o_st + c, y);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Pack<T, V>*>(st + j * p.C) = raw[j + 1];
+  for (int j = 0; j < W - 1; ++j) raw[j + 1].store(st + j * p.C);
 }
 
 // ---------------------------------------------------------------- backward
@@ -294,12 +294,12 @@ __global__ void __launch_bounds__(NTHREADS) conv_bwd_kernel(BwdParams p) {
       }
       const int64_t stop = hi + W - 1;
       for (int64_t t = lo; t < stop; t += KT) {
-        Pack<T, V> rx[KT], rd[KT];
+        Vec<T, V> rx[KT], rd[KT];
 #pragma unroll
         for (int k = 0; k < KT; ++k)
           if (t + k < stop && t + k < end) {
-            rx[k] = *reinterpret_cast<const Pack<T, V>*>(x + (t + k) * p.x_st + c);
-            rd[k] = *reinterpret_cast<const Pack<T, V>*>(dout + (t + k) * p.d_st + c);
+            rx[k].load(x + (t + k) * p.x_st + c);
+            rd[k].load(dout + (t + k) * p.d_st + c);
           }
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(NTHREADS) conv_bwd_kernel(BwdParams p) {
             float dy[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-              win[W - 1 + k][v] = to_f32(rx[k].v[v]);
-              dy[v] = to_f32(rd[k].v[v]);
+              win[W - 1 + k][v] = rx[k].get(v);
+              dy[v] = rd[k].get(v);
             }
             pre_gradient<V, W>(now, dy, &win[k], w, b, p.silu);
             if (t + k < hi) {
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(NTHREADS) conv_bwd_kernel(BwdParams p) {
 }
 
 // The blocks' sums in order: dw[c][j] and dbias[c].
-__global__ void __launch_bounds__(NTHREADS) conv_reduce_kernel(const float* part, int64_t blocks, int W, int64_t C,
+static __global__ void __launch_bounds__(NTHREADS) conv_reduce_kernel(const float* part, int64_t blocks, int W, int64_t C,
                                                               float* dw, float* db) {
   const int64_t c = static_cast<int64_t>(blockIdx.x) * NTHREADS + threadIdx.x;
   const int j = blockIdx.y;

@@ -35,6 +35,7 @@ int io_bytes(kda_dtype_t dt) { return dt == KDA_F32 ? 4 : dt == KDA_BF16 || dt =
 struct RowView {
   void* data = nullptr;
   int64_t st = 0, sg = 0;
+  int eb = 1;               // bytes per element
   Span span{0, 0, 0, 0};
 };
 
@@ -57,6 +58,7 @@ kda_status_t view_rows(const kda_tensor_t* t, kda_dtype_t dt, int64_t T, int64_t
   if (!t->data) return KDA_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(t->data) % eb != 0) return KDA_ERR_ALIGN;
   v->data = t->data;
+  v->eb = eb;
   v->span = {reinterpret_cast<uintptr_t>(t->data), T, v->st * eb, extent * eb};
   return KDA_OK;
 }
@@ -106,25 +108,18 @@ kda_status_t check_packing_args(const int32_t* cu, int32_t num_seqs, int64_t T) 
   return KDA_OK;
 }
 
-// Rows of `v` can be moved 16 bytes at a time.
-bool wide(const RowView& v, int eb) {
-  return reinterpret_cast<uintptr_t>(v.data) % 16 == 0 && v.st * eb % 16 == 0 && v.sg * eb % 16 == 0;
+// The rows of `v` start at multiples of `bytes`.
+bool aligned(const RowView& v, int64_t bytes) {
+  return v.span.at % bytes == 0 && v.span.step % bytes == 0 && v.sg * v.eb % bytes == 0;
 }
 bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// f(element, vector width) for the type and whether 16-byte accesses are possible
+// f(the launches of the type)
 template <typename F>
-void by_type(kda_dtype_t dt, bool vec, F f) {
-  if (dt == KDA_BF16) {
-    if (vec) f(__nv_bfloat16(), std::integral_constant<int, 8>());
-    else f(__nv_bfloat16(), std::integral_constant<int, 1>());
-  } else if (dt == KDA_F16) {
-    if (vec) f(__half(), std::integral_constant<int, 8>());
-    else f(__half(), std::integral_constant<int, 1>());
-  } else {
-    if (vec) f(float(), std::integral_constant<int, 4>());
-    else f(float(), std::integral_constant<int, 1>());
-  }
+cudaError_t by_type(kda_dtype_t dt, F f) {
+  if (dt == KDA_BF16) return f(kda::Mixer<__nv_bfloat16>());
+  if (dt == KDA_F16) return f(kda::Mixer<__half>());
+  return f(kda::Mixer<float>());
 }
 
 // ------------------------------------------------------------- convolution
@@ -160,13 +155,6 @@ kda_status_t check_conv(const kda_tensor_t* x, const kda_tensor_t* weight, const
   return KDA_OK;
 }
 
-template <typename F>
-void by_width(int W, F f) {
-  if (W == 2) f(std::integral_constant<int, 2>());
-  else if (W == 3) f(std::integral_constant<int, 3>());
-  else f(std::integral_constant<int, 4>());
-}
-
 // Tokens per warp: enough warps to fill the device, in steps of `unit` tokens
 // and at most `most`.
 int64_t conv_run(int64_t T, int64_t channel_blocks, int dev, int unit, int most) {
@@ -198,7 +186,7 @@ kda_status_t kda_conv_fwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   int dev = 0;
   if ((st = prologue(&dev)) != KDA_OK) return st;
   const int eb = io_bytes(a.dt), V = 16 / eb;
-  const bool vec = a.C % V == 0 && wide(a.x, eb) && wide(a.out, eb) && wide(init) && wide(fin);
+  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && wide(init) && wide(fin);
   const int64_t cb = (a.C + 32 * (vec ? V : 1) - 1) / (32 * (vec ? V : 1));
   cv::Params p;
   p.x = a.x.data;
@@ -217,12 +205,7 @@ kda_status_t kda_conv_fwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   p.N = num_seqs;
   p.silu = activation == KDA_ACT_SILU;
   const dim3 grid(static_cast<unsigned>(p.run_blocks + (num_seqs + cv::NWARPS - 1) / cv::NWARPS), static_cast<unsigned>(cb));
-  by_type(a.dt, vec, [&](auto t, auto v) {
-    by_width(a.W, [&](auto w) {
-      cv::conv_fwd_kernel<decltype(t), v.value, w.value><<<grid, cv::NTHREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    });
-  });
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = by_type(a.dt, [&](auto m) { return m.conv_fwd(p, a.W, vec, grid, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
 
@@ -252,7 +235,7 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
   if ((st = prologue(&dev)) != KDA_OK) return st;
   if (B == 0) return KDA_OK;
   const int eb = io_bytes(a.dt), V = 16 / eb;
-  const bool vec = a.C % V == 0 && wide(a.x, eb) && wide(a.out, eb) && wide(sp);
+  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && wide(sp);
   cv::DecodeParams p;
   p.x = a.x.data;
   p.weight = static_cast<const float*>(a.weight);
@@ -268,13 +251,7 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
   p.silu = activation == KDA_ACT_SILU;
   const int per = cv::NTHREADS * (vec ? V : 1);
   const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((a.C + per - 1) / per));
-  by_type(a.dt, vec, [&](auto t, auto v) {
-    by_width(a.W, [&](auto w) {
-      cv::conv_decode_kernel<decltype(t), v.value, w.value>
-          <<<grid, cv::NTHREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    });
-  });
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = by_type(a.dt, [&](auto m) { return m.conv_decode(p, a.W, vec, grid, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
 
@@ -306,7 +283,7 @@ kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   if ((st = prologue(&dev)) != KDA_OK) return st;
   if ((st = prepare_pool(dev)) != KDA_OK) return st;
   const int eb = io_bytes(a.dt), V = 16 / eb;
-  const bool vec = a.C % V == 0 && wide(a.x, eb) && wide(a.out, eb) && wide(g, eb) && wide(init) && wide(dfin) &&
+  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && aligned(g, 16) && wide(init) && wide(dfin) &&
                    wide(dinit);
   const int64_t cb = (a.C + 32 * (vec ? V : 1) - 1) / (32 * (vec ? V : 1));
   cv::BwdParams p;
@@ -334,14 +311,12 @@ kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   if (e != cudaSuccess) return cuda_fail(e);
   p.part = static_cast<float*>(part);
   const dim3 grid(static_cast<unsigned>(p.run_blocks + (num_seqs + cv::NWARPS - 1) / cv::NWARPS), static_cast<unsigned>(cb));
-  by_type(a.dt, vec, [&](auto t, auto v) {
-    by_width(a.W, [&](auto w) {
-      cv::conv_bwd_kernel<decltype(t), v.value, w.value><<<grid, cv::NTHREADS, 0, cs>>>(p);
-    });
-  });
-  cv::conv_reduce_kernel<<<dim3(static_cast<unsigned>((a.C + cv::NTHREADS - 1) / cv::NTHREADS), a.W + 1), cv::NTHREADS, 0, cs>>>(
+  e = by_type(a.dt, [&](auto m) { return m.conv_bwd(p, a.W, vec, grid, cs); });
+  if (e == cudaSuccess) {
+    cv::conv_reduce_kernel<<<dim3(static_cast<unsigned>((a.C + cv::NTHREADS - 1) / cv::NTHREADS), a.W + 1), cv::NTHREADS, 0, cs>>>(
       p.part, p.run_blocks, a.W, a.C, static_cast<float*>(dw), static_cast<float*>(db));
-  e = cudaGetLastError();
+    e = cudaGetLastError();
+  }
   const cudaError_t ef = cudaFreeAsync(part, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   return ef != cudaSuccess ? cuda_fail(ef) : KDA_OK;

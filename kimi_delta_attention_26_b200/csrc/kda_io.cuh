@@ -8,10 +8,101 @@
 
 namespace kda {
 
-// V consecutive elements of a row, moved as one access.
+// V consecutive elements of a row, moved as one access of 2, 4, 8 or 16 bytes.
+// Held as 32-bit words: as 16-bit members the compiler moves them one by one.
+template <int BYTES>
+struct Words;
+template <>
+struct Words<2> { using type = uint16_t; };
+template <>
+struct Words<4> { using type = uint32_t; };
+template <>
+struct Words<8> { using type = uint2; };
+template <>
+struct Words<16> { using type = uint4; };
+
+template <typename T>
+__device__ __forceinline__ float lo_f32(uint32_t w);
+template <typename T>
+__device__ __forceinline__ float hi_f32(uint32_t w);
+template <>
+__device__ __forceinline__ float lo_f32<__nv_bfloat16>(uint32_t w) { return __uint_as_float(w << 16); }
+template <>
+__device__ __forceinline__ float hi_f32<__nv_bfloat16>(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+template <>
+__device__ __forceinline__ float lo_f32<__half>(uint32_t w) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+}
+template <>
+__device__ __forceinline__ float hi_f32<__half>(uint32_t w) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16)));
+}
+template <>
+__device__ __forceinline__ float lo_f32<float>(uint32_t w) { return __uint_as_float(w); }
+
+template <typename T>
+__device__ __forceinline__ uint32_t pair_bits(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pair_bits<__nv_bfloat16>(float lo, float hi) { return pack_bf16(lo, hi); }
+template <>
+__device__ __forceinline__ uint32_t pair_bits<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+
 template <typename T, int V>
-struct alignas(sizeof(T) * V) Pack {
-  T v[V];
+struct Vec {
+  static constexpr int BYTES = V * sizeof(T);
+  using Raw = typename Words<BYTES>::type;
+  Raw raw;
+
+  __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const Raw*>(p); }
+  __device__ __forceinline__ void store(void* p) const { *static_cast<Raw*>(p) = raw; }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    if constexpr (BYTES <= 4) return raw;
+    else if constexpr (BYTES == 8) return i == 0 ? raw.x : raw.y;
+    else return i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w;
+  }
+  __device__ __forceinline__ void set_word(int i, uint32_t w) {
+    if constexpr (BYTES <= 4) raw = static_cast<Raw>(w);
+    else if constexpr (BYTES == 8) (i == 0 ? raw.x : raw.y) = w;
+    else (i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w) = w;
+  }
+  __device__ __forceinline__ float get(int i) const {  // i known at compile time
+    if constexpr (sizeof(T) == 4) return __uint_as_float(word(i));
+    else return i % 2 ? hi_f32<T>(word(i / 2)) : lo_f32<T>(word(i / 2));
+  }
+  __device__ __forceinline__ void get(float (&x)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = get(i);
+  }
+  __device__ __forceinline__ void set(const float (&x)[V]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) set_word(i, __float_as_uint(x[i]));
+    } else if constexpr (V == 1) {
+      set_word(0, pair_bits<T>(x[0], 0.f));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) set_word(i / 2, pair_bits<T>(x[i], x[i + 1]));
+    }
+  }
+  // the first `valid` elements one by one, zeros for the others
+  __device__ __forceinline__ void load_some(const T* p, int valid) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) set_word(i, i < valid ? reinterpret_cast<const uint32_t*>(p)[i] : 0u);
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const uint32_t lo = i < valid ? h[i] : 0u, hi = i + 1 < valid && i + 1 < V ? h[i + 1] : 0u;
+        set_word(i / 2, lo | hi << 16);
+      }
+    }
+  }
 };
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -29,17 +120,16 @@ __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2hal
 
 template <typename T, int V>
 __device__ __forceinline__ void load_f32(float (&x)[V], const T* p) {
-  const Pack<T, V> a = *reinterpret_cast<const Pack<T, V>*>(p);
-#pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = to_f32(a.v[i]);
+  Vec<T, V> a;
+  a.load(p);
+  a.get(x);
 }
 
 template <typename T, int V>
 __device__ __forceinline__ void store_f32(T* p, const float (&x)[V]) {
-  Pack<T, V> a;
-#pragma unroll
-  for (int i = 0; i < V; ++i) a.v[i] = from_f32<T>(x[i]);
-  *reinterpret_cast<Pack<T, V>*>(p) = a;
+  Vec<T, V> a;
+  a.set(x);
+  a.store(p);
 }
 
 // sigmoid, x sigmoid(x) and its derivative. exp(-x) overflows to infinity for

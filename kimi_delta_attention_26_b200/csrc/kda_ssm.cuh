@@ -13,9 +13,13 @@
 namespace kda {
 namespace ssm {
 
-constexpr int NTHREADS = 128;
-constexpr int S = 4;    // states per thread
-constexpr int TT = 16;  // tokens per tile
+constexpr int NTHREADS = 128;  // consumers of the forward scan; the other kernels' blocks
+constexpr int KT = 16;         // tokens between kept states (the gradients' tiles)
+constexpr int STAGES = 3;      // tiles of steps, B and C in flight
+constexpr int YSLOTS = 2;      // tiles of outputs in flight
+
+// Threads that share a channel's N states, at most four each.
+inline int threads_per_channel(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
 
 struct Params {
   const void* u;
@@ -30,17 +34,17 @@ struct Params {
   const float* init;        // [NS, C, N] or null
   void* out;
   float* fin;               // [NS, C, N] or null
-  float* ck;                // states before each tile, or null
+  float* ck;                // states before every KT tokens of a sequence, or null
+  float* carry;             // time split: [ranges, C, N] each range's last state, else null
+  float* sum_d;             // and [ranges, C] the sum of its steps
   int64_t T;
+  int64_t run;              // time split: tokens per range, else 0 (a range is a sequence)
   int64_t u_st, dt_st, z_st, o_st, b_st, b_sg, c_st, c_sg;  // element strides over tokens and groups
   int NS, C, N, G;          // sequences, channels, states, groups
   int blocks_per_group;     // channel blocks of a group
   int softplus;
+  int wide;                 // bits 0..5: rows of u, dt, z, B, C, out can be moved in pieces (u, dt, z, out: 2; B, C: S)
 };
-
-__device__ __forceinline__ float step_of(float r, int softplus) {
-  return softplus ? (r > 20.f ? r : log1pf(expf(r))) : r;
-}
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -50,102 +54,411 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The tiles of all sequences are numbered from start / TT + seq on: distinct,
-// and at most T / TT + NS of them.
-__device__ __forceinline__ int64_t first_tile(int64_t start, int seq) { return start / TT + seq; }
+// The step: log(1 + exp(r)) = max(r, 0) + log1p(e) with e = exp(-|r|) in (0, 1],
+// and log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3. atanh(s) / s as a
+// polynomial in w = s^2 <= 1/9, of degree 6: its series to w^5 / 11 with the
+// rest's size at w = 1/9 in the last term (below 2^-26 off).
+// EXACT (fp32 inputs): exp's argument in two parts; as one its rounding costs
+// |r| 2^-24 of the step, which 16-bit inputs do not show.
+template <bool EXACT>
+__device__ __forceinline__ float step_of(float r, int softplus) {
+  if (!softplus) return r;
+  const float m = -fabsf(r), x = m * kLog2e;
+  float e = exp2_approx(x);
+  if (EXACT) {
+    const float rest = fmaf(m, kLog2e, -x) + m * 1.925963033500234e-8f;  // log2(e) less its nearest fp32
+    e = fmaf(e * 0.6931471805599453f, rest, e);
+  }
+  const float s = __fdividef(e, 2.f + e), w = s * s;
+  float t = fmaf(w, 1.f / 12, 1.f / 11);
+  t = fmaf(w, t, 1.f / 9);
+  t = fmaf(w, t, 1.f / 7);
+  t = fmaf(w, t, 1.f / 5);
+  t = fmaf(w, t, 1.f / 3);
+  t = fmaf(w, t, 1.f);
+  return fmaf(2.f * s, t, fmaxf(r, 0.f));
+}
 
-// One sequence and 128 / L channels per block, L threads of S states per channel.
-template <typename T, int L, bool OUT>
-__global__ void __launch_bounds__(NTHREADS) ssm_fwd_kernel(Params p) {
-  constexpr int CH = NTHREADS / L, NP = L * S;
-  __shared__ float2 s_d[TT][CH];
-  __shared__ __align__(16) float s_b[TT][NP], s_c[TT][NP];
-  __shared__ float s_y[TT][CH];
-  const int tid = threadIdx.x, q = tid % L, ch = tid / L;
-  const int seq = blockIdx.y;
+// exp2 of a pair; pairs are multiplied and added as one instruction (half the
+// instructions, the same time on the multiply-add pipe)
+__device__ __forceinline__ float2 pexp2(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
+
+// S values at p as pairs (S = 1: the second half is 0)
+template <int S>
+__device__ __forceinline__ void load_pairs(float2 (&x)[(S + 1) / 2], const float* p) {
+  if constexpr (S == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = make_float2(v.x, v.y);
+    x[1] = make_float2(v.z, v.w);
+  } else if constexpr (S == 2) {
+    x[0] = *reinterpret_cast<const float2*>(p);
+  } else {
+    x[0] = make_float2(*p, 0.f);
+  }
+}
+
+// The kept states of all sequences are numbered from start / KT + seq on:
+// distinct, and at most T / KT + NS of them.
+__device__ __forceinline__ int64_t first_kept(int64_t start, int seq) { return start / KT + seq; }
+
+// A range's pieces of sequences, in order: f(seq, start, end, lo, hi) for the
+// tokens [lo, hi) of the sequence [start, end). A range is a sequence, or, with
+// the time split, `run` tokens of the packed batch. `last_cut` visits only the
+// piece that goes on in the next range.
+template <typename F>
+__device__ __forceinline__ void for_pieces(const Params& p, int range, bool last_cut, F f) {
+  if (!p.run) {
+    const int64_t start = bound(p.cu, range, p.T), end = max(start, bound(p.cu, range + 1, p.T));
+    f(range, start, end, start, end);
+    return;
+  }
+  const int64_t r0 = range * p.run, r1 = min(r0 + p.run, p.T);
+  int64_t pos = r0;
+  for (int s = first_sequence(p.cu, p.NS, last_cut ? r1 - 1 : r0); s < p.NS; ++s) {
+    const int64_t start = bound(p.cu, s, p.T), end = bound(p.cu, s + 1, p.T);
+    if (start >= r1) break;
+    const int64_t lo = max(start, pos), hi = min(end, r1);
+    if (hi <= lo) continue;
+    pos = hi;
+    if (!last_cut || end > r1) f(s, start, end, lo, hi);
+  }
+}
+
+// K rows of V elements, the rows base + row(k) * st. `all`: one access each; else
+// the `valid` first elements one by one, zeros for the others. One branch for
+// all rows, so that their loads are in flight together.
+template <typename T, int V, int K, typename R>
+__device__ __forceinline__ void load_rows(Vec<T, V> (&x)[K], const T* base, int64_t st, int valid, bool all, R row) {
+  if (all) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k].load(base + row(k) * st);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k].load_some(base + row(k) * st, valid);
+  }
+}
+
+constexpr int ROLE = NTHREADS;              // threads that make tiles; as many finish outputs
+
+// Two shapes of the forward scan. DEEP: one block per SM, longer tiles and more
+// straight-line code, for grids that give an SM no second block; else two
+// blocks per SM share it.
+template <typename T, int L, int S, int CH, bool DEEP>
+struct FwdShared {
+  static constexpr int TT = DEEP ? 64 : 32;  // tokens per tile
+  static constexpr int GT = DEEP ? 16 : 8;   // tokens of straight-line code in the states' loop
+  static constexpr int STATE_THREADS = CH * L, THREADS = STATE_THREADS + 2 * ROLE;
+  // The parts of the outputs: 16 bytes (four tokens) per thread and four
+  // tokens, even channels before odd ones. The strides put the eight threads
+  // of a store and of a load into different banks.
+  static constexpr int ODD = CH / 2 * 16 + 64, QS = 2 * ODD + 16;
+  float2 d[STAGES][TT][CH];        // d, d u
+  alignas(16) float b[STAGES][TT][L * S], c[STAGES][TT][L * S];
+  alignas(16) unsigned char y[YSLOTS][TT / 4][L][QS];
+  unsigned long long full[STAGES], empty[STAGES], y_full[YSLOTS], y_empty[YSLOTS];
+};
+
+// A ring of `n` slots: the slot in use and the parity of its current round.
+template <int n>
+struct Ring {
+  int slot = 0;
+  uint32_t phase;
+  __device__ explicit Ring(uint32_t first) : phase(first) {}
+  __device__ __forceinline__ void next() {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// 128 / L channels of one range of tokens per block, in three roles of four
+// warps: the states (L threads of S states per channel, one token after
+// another), the tiles (TT tokens of d, d u, B and C into shared memory, a ring
+// of STAGES) and the outputs (D u, the gate).
+// OUT: the outputs; else states only, for the gradients (ck) or the time split (carry).
+template <typename T, int L, int S, int CH, bool OUT, bool DEEP>
+__global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ? 1 : 2) ssm_fwd_kernel(Params p) {
+  using Sh = FwdShared<T, L, S, CH, DEEP>;
+  constexpr int SN = Sh::STATE_THREADS, TT = Sh::TT, GT = Sh::GT;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Sh& sm = *reinterpret_cast<Sh*>(smem);
+  const int role = threadIdx.x < SN ? 0 : 1 + (threadIdx.x - SN) / ROLE;
+  const int tid = role == 0 ? threadIdx.x : (threadIdx.x - SN) % ROLE;
+  const int range = blockIdx.y;
   const int group = blockIdx.x / p.blocks_per_group, cg = p.C / p.G;
   const int c0 = group * cg + (blockIdx.x % p.blocks_per_group) * CH, c_end = min(c0 + CH, (group + 1) * cg);
-  if (blockIdx.x == 0 && tid == 0) check_packing(p.cu, seq, p.T);
-  const int64_t start = bound(p.cu, seq, p.T), end = bound(p.cu, seq + 1, p.T);
-  const T* u = static_cast<const T*>(p.u);
-  const T* dt = static_cast<const T*>(p.dt);
-  const T* z = static_cast<const T*>(p.z);
-  const T* bb = static_cast<const T*>(p.b) + group * p.b_sg;
-  const T* cc = static_cast<const T*>(p.c) + group * p.c_sg;
-  const bool live = c0 + ch < c_end;
-  float a[S], h[S];
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const int n = q * S + i;
-    const int64_t at = static_cast<int64_t>(c0 + ch) * p.N + n;
-    a[i] = live && n < p.N ? p.A[at] * kLog2e : 0.f;
-    h[i] = live && n < p.N && p.init ? p.init[static_cast<int64_t>(seq) * p.C * p.N + at] : 0.f;
-  }
-  int64_t tile = first_tile(start, seq);
-  for (int64_t t0 = start; t0 < end; t0 += TT, ++tile) {
-    const int nt = static_cast<int>(min(static_cast<int64_t>(TT), end - t0));
-    __syncthreads();
-    for (int i = tid; i < TT * CH; i += NTHREADS) {
-      const int t = i / CH, k = i % CH;
-      float2 v = make_float2(0.f, 0.f);
-      if (t < nt && c0 + k < c_end) {
-        const float r = to_f32(dt[(t0 + t) * p.dt_st + c0 + k]) + (p.dt_bias ? p.dt_bias[c0 + k] : 0.f);
-        v.x = step_of(r, p.softplus);
-        v.y = v.x * to_f32(u[(t0 + t) * p.u_st + c0 + k]);
-      }
-      s_d[t][k] = v;
+  const bool split_pass = !OUT && p.carry;  // the time split's first pass: the piece that goes on
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&sm.full[i], ROLE / 32);
+      mbar_init(&sm.empty[i], SN / 32);
     }
-    for (int i = tid; i < TT * NP; i += NTHREADS) {
-      const int t = i / NP, n = i % NP;
-      const bool in = t < nt && n < p.N;
-      s_b[t][n] = in ? to_f32(bb[(t0 + t) * p.b_st + n]) : 0.f;
-      if (OUT) s_c[t][n] = in ? to_f32(cc[(t0 + t) * p.c_st + n]) : 0.f;
-    }
-    __syncthreads();
-    if (!OUT && live) {
-#pragma unroll
-      for (int i = 0; i < S; ++i)
-        if (q * S + i < p.N) p.ck[(tile * p.C + c0 + ch) * p.N + q * S + i] = h[i];
-    }
-    for (int t = 0; t < nt; ++t) {
-      const float2 d = s_d[t][ch];
-      const float4 b4 = *reinterpret_cast<const float4*>(&s_b[t][q * S]);
-      const float bv[S] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-      for (int i = 0; i < S; ++i) h[i] = fmaf(exp2_approx(d.x * a[i]), h[i], d.y * bv[i]);
-      if (OUT) {
-        const float4 c4 = *reinterpret_cast<const float4*>(&s_c[t][q * S]);
-        float y = c4.x * h[0];
-        y = fmaf(c4.y, h[1], y);
-        y = fmaf(c4.z, h[2], y);
-        y = fmaf(c4.w, h[3], y);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (q == 0) s_y[t][ch] = y;
-      }
-    }
-    if (OUT) {
-      __syncthreads();
-      for (int i = tid; i < nt * CH; i += NTHREADS) {
-        const int t = i / CH, k = i % CH;
-        if (c0 + k >= c_end) continue;
-        float y = s_y[t][k];
-        if (p.D) y = fmaf(p.D[c0 + k], to_f32(u[(t0 + t) * p.u_st + c0 + k]), y);
-        if (z) y *= silu(to_f32(z[(t0 + t) * p.z_st + c0 + k]));
-        static_cast<T*>(p.out)[(t0 + t) * p.o_st + c0 + k] = from_f32<T>(y);
-      }
+    for (int i = 0; i < YSLOTS; ++i) {
+      mbar_init(&sm.y_full[i], SN / 32);
+      mbar_init(&sm.y_empty[i], ROLE / 32);
     }
   }
-  if (p.fin && live) {
+  if (!split_pass && blockIdx.x == 0 && range == 0)
+    for (int s = threadIdx.x; s < p.NS; s += Sh::THREADS) check_packing(p.cu, s, p.T);
+  __syncthreads();
+  if (role == 0) {  // -------------------------------------------- the states
+    // Lanes: bit 1 (and the highest bits) the channel, the others the channel's
+    // thread q. Wide loads from shared memory take half the time where lanes
+    // that differ in bit 0 alone, or in bit 1 alone, read the same address: of
+    // B and C the latter, of d the former (measured: 2 and 1 clocks, not 4 and 2).
+    const int lane = tid % 32, rest = (lane & 1) | (lane >> 2 << 1);
+    const int q = L == 32 ? lane : rest % L;
+    const int ch = tid / 32 * (32 / L) + (L == 32 ? 0 : (lane >> 1 & 1) | rest / L << 1);
+    const bool live = c0 + ch < c_end;
+    constexpr int H = (S + 1) / 2;  // pairs
+    float2 a[H], h[H];
+    float av[2 * H], hv[2 * H];
+    const int64_t row = static_cast<int64_t>(c0 + ch) * p.N + q * S, cn = static_cast<int64_t>(p.C) * p.N;
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      const int n = q * S + i;
-      if (n < p.N) p.fin[(static_cast<int64_t>(seq) * p.C + c0 + ch) * p.N + n] = h[i];
+    for (int i = 0; i < 2 * H; ++i) av[i] = i < S && live && q * S + i < p.N ? p.A[row + i] * kLog2e : 0.f;
+#pragma unroll
+    for (int i = 0; i < H; ++i) a[i] = make_float2(av[2 * i], av[2 * i + 1]);
+    Ring<STAGES> in(0);
+    Ring<YSLOTS> yr(1);
+    for_pieces(p, range, split_pass, [&](int seq, int64_t start, int64_t end, int64_t lo, int64_t hi) {
+      const int64_t at = seq * cn + row;
+#pragma unroll
+      for (int i = 0; i < 2 * H; ++i) {
+        const bool on = i < S && live && q * S + i < p.N;
+        hv[i] = on && p.init && lo == start ? p.init[at + i] : 0.f;
+        if (on && p.run && !split_pass && lo > start) {
+          // the state before this range: those of the ranges since the sequence's start, decayed
+          for (int64_t r = start / p.run; r < range; ++r)
+            hv[i] = fmaf(r * p.run <= start ? 0.f : exp2_approx(av[i] * p.sum_d[r * p.C + c0 + ch]), hv[i],
+                         p.carry[r * cn + row + i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < H; ++i) h[i] = make_float2(hv[2 * i], hv[2 * i + 1]);
+      float sum = 0.f;
+      for (int64_t t0 = lo; t0 < hi; t0 += TT) {
+        const int nt = static_cast<int>(min(static_cast<int64_t>(TT), hi - t0));
+        mbar_wait(&sm.full[in.slot], in.phase);
+        if (OUT) mbar_wait(&sm.y_empty[yr.slot], yr.phase);
+        const float2* dp = &sm.d[in.slot][0][ch];
+        const float* bp = &sm.b[in.slot][0][q * S];
+        const float* cp = &sm.c[in.slot][0][q * S];
+        unsigned char* yp = &sm.y[yr.slot][0][q][ch % 2 * Sh::ODD + ch / 2 * 16];
+        for (int t = 0; t < nt; t += GT, dp += GT * CH, bp += GT * L * S, cp += GT * L * S, yp += GT / 4 * L * Sh::QS) {
+          if (!OUT && p.ck && t % KT == 0 && live) {  // the state before token t, for the gradients
+            const int64_t k = (first_kept(start, seq) + (t0 - start + t) / KT) * cn + row;
+#pragma unroll
+            for (int i = 0; i < H; ++i) hv[2 * i] = h[i].x, hv[2 * i + 1] = h[i].y;
+            if (S == 4 && p.N % 4 == 0) {
+              if (q * S < p.N) *reinterpret_cast<float4*>(p.ck + k) = make_float4(hv[0], hv[1], hv[2 % (2 * H)], hv[3 % (2 * H)]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < S; ++i)
+                if (q * S + i < p.N) p.ck[k + i] = hv[i];
+            }
+          }
+          float y[GT];
+#pragma unroll
+          for (int j = 0; j < GT; ++j) {  // past the piece's end d = 0: the state stays
+            const float2 d = dp[j * CH];
+            float2 b[H], c[H], acc;
+            load_pairs<S>(b, bp + j * L * S);
+            if (OUT) load_pairs<S>(c, cp + j * L * S);
+            const float2 dd = make_float2(d.x, d.x), du = make_float2(d.y, d.y);
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              h[i] = __ffma2_rn(pexp2(__fmul2_rn(dd, a[i])), h[i], __fmul2_rn(du, b[i]));
+              if (OUT) acc = i ? __ffma2_rn(c[i], h[i], acc) : __fmul2_rn(c[i], h[i]);
+            }
+            if (OUT) y[j] = S > 1 ? acc.x + acc.y : acc.x;
+            if (split_pass) sum += d.x;
+          }
+          if (OUT) {
+#pragma unroll
+            for (int j = 0; j < GT; j += 4)
+              *reinterpret_cast<float4*>(yp + j / 4 * L * Sh::QS) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+          }
+        }
+        mbar_arrive_warp(&sm.empty[in.slot]);
+        if (OUT) mbar_arrive_warp(&sm.y_full[yr.slot]);
+        in.next();
+        yr.next();
+      }
+#pragma unroll
+      for (int i = 0; i < H; ++i) hv[2 * i] = h[i].x, hv[2 * i + 1] = h[i].y;
+      float* to = split_pass ? p.carry + range * cn + row : hi == end && p.fin ? p.fin + at : nullptr;
+      if (live && to) {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+          if (q * S + i < p.N) to[i] = hv[i];
+      }
+      if (split_pass && live && q == 0) p.sum_d[static_cast<int64_t>(range) * p.C + c0 + ch] = sum;
+    });
+    if (p.run && !split_pass && range == 0 && p.fin && live) {  // sequences without tokens
+      for (int s = 0; s < p.NS; ++s) {
+        if (bound(p.cu, s + 1, p.T) > bound(p.cu, s, p.T)) continue;
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+          if (q * S + i < p.N) p.fin[s * cn + row + i] = p.init ? p.init[s * cn + row + i] : 0.f;
+      }
     }
+    return;
+  }
+  // a thread's part of a tile: two channels of every TK-th token
+  constexpr int ROWT = CH / 2, TK = ROLE / ROWT, NU = (TT + TK - 1) / TK;
+  const int k0 = tid % ROWT * 2, tk = tid / ROWT, valid = max(0, min(2, c_end - c0 - k0));
+  if (role == 1) {  // --------------------------------------------- the tiles
+    const T* u = static_cast<const T*>(p.u) + c0 + k0;
+    const T* dt = static_cast<const T*>(p.dt) + c0 + k0;
+    const T* bb = static_cast<const T*>(p.b) + group * p.b_sg;
+    const T* cc = static_cast<const T*>(p.c) + group * p.c_sg;
+    float bias[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) bias[i] = p.dt_bias && i < valid ? p.dt_bias[c0 + k0 + i] : 0.f;
+    constexpr int NB = (TT * L + ROLE - 1) / ROLE;
+    Vec<T, 2> ru[NU], rd[NU];
+    Vec<T, S> rb[NB], rc[NB];
+    // rows past the piece's end: its last one again, set to 0 below
+    const int n0 = tid % L * S, nv = max(0, min(S, p.N - n0));
+    auto load = [&](int64_t t0, int nt) {
+      auto tok = [&](int k) { return t0 + min(tk + k * TK, nt - 1); };
+      auto bct = [&](int k) { return t0 + min((tid + k * ROLE) / L, nt - 1); };
+      load_rows(ru, u, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
+      load_rows(rd, dt, p.dt_st, valid, (p.wide & 2) && valid == 2, tok);
+      load_rows(rb, bb + n0, p.b_st, nv, (p.wide & 8) && nv == S, bct);
+      if (OUT) load_rows(rc, cc + n0, p.c_st, nv, (p.wide & 16) && nv == S, bct);
+    };
+    Ring<STAGES> to(1);
+    for_pieces(p, range, split_pass, [&](int, int64_t, int64_t, int64_t lo, int64_t hi) {
+      if (lo < hi) load(lo, static_cast<int>(min(static_cast<int64_t>(TT), hi - lo)));
+      for (int64_t t0 = lo; t0 < hi; t0 += TT) {
+        const int nt = static_cast<int>(min(static_cast<int64_t>(TT), hi - t0));
+        // this tile's; the next one's loads go out before its arithmetic
+        Vec<T, 2> tu[NU], td[NU];
+        float wb[NB][S], wc[NB][S];
+#pragma unroll
+        for (int k = 0; k < NU; ++k) {
+          tu[k] = ru[k];
+          td[k] = rd[k];
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+#pragma unroll
+          for (int i = 0; i < S; ++i) {
+            wb[k][i] = rb[k].get(i);
+            if (OUT) wc[k][i] = rc[k].get(i);
+          }
+          if (nt < TT && (tid + k * ROLE) / L >= nt) {
+#pragma unroll
+            for (int i = 0; i < S; ++i) wb[k][i] = wc[k][i] = 0.f;
+          }
+        }
+        if (t0 + TT < hi) load(t0 + TT, static_cast<int>(min(static_cast<int64_t>(TT), hi - t0 - TT)));
+        float2 v[NU][2];
+        const bool short_tile = nt < TT || valid < 2;
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float d = step_of<sizeof(T) == 4>(td[k].get(i) + bias[i], p.softplus);
+            v[k][i] = make_float2(d, d * tu[k].get(i));
+            if (short_tile && (tk + k * TK >= nt || i >= valid)) v[k][i] = make_float2(0.f, 0.f);
+          }
+        mbar_wait(&sm.empty[to.slot], to.phase);
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+          if (TT % TK == 0 || tk + k * TK < TT)
+            *reinterpret_cast<float4*>(&sm.d[to.slot][tk + k * TK][k0]) =
+                make_float4(v[k][0].x, v[k][0].y, v[k][1].x, v[k][1].y);
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+          if (TT * L % ROLE == 0 || tid + k * ROLE < TT * L) {
+            const int i = tid + k * ROLE;
+            store_f32<float, S>(&sm.b[to.slot][i / L][i % L * S], wb[k]);
+            if (OUT) store_f32<float, S>(&sm.c[to.slot][i / L][i % L * S], wc[k]);
+          }
+        mbar_arrive_warp(&sm.full[to.slot]);
+        to.next();
+      }
+    });
+    return;
+  }
+  if (OUT) {  // -------------------------------------------------- the outputs
+    // a thread's part of a tile: two channels of four tokens, of every GK-th four
+    constexpr int GK = ROLE / ROWT, NG = (TT / 4 + GK - 1) / GK;
+    const T* u = static_cast<const T*>(p.u) + c0 + k0;
+    const T* z = static_cast<const T*>(p.z) + c0 + k0;
+    T* out = static_cast<T*>(p.out) + c0 + k0;
+    float skip[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) skip[i] = p.D && i < valid ? p.D[c0 + k0 + i] : 0.f;
+    Vec<T, 2> ru[4 * NG], rz[4 * NG];
+    auto load = [&](int64_t t0, int nt) {
+      auto tok = [&](int k) { return t0 + min((tk + k / 4 * GK) * 4 + k % 4, nt - 1); };
+      if (p.D) load_rows(ru, u, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
+      if (p.z) load_rows(rz, z, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
+    };
+    Ring<YSLOTS> yr(0);
+    for_pieces(p, range, split_pass, [&](int, int64_t, int64_t, int64_t lo, int64_t hi) {
+      if (lo < hi) load(lo, static_cast<int>(min(static_cast<int64_t>(TT), hi - lo)));
+      for (int64_t t0 = lo; t0 < hi; t0 += TT) {
+        const int nt = static_cast<int>(min(static_cast<int64_t>(TT), hi - t0));
+        float du[4 * NG][2], gate[4 * NG][2];
+#pragma unroll
+        for (int k = 0; k < 4 * NG; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            du[k][i] = p.D ? skip[i] * ru[k].get(i) : 0.f;
+            gate[k][i] = p.z ? silu(rz[k].get(i)) : 1.f;
+          }
+        if (t0 + TT < hi) load(t0 + TT, static_cast<int>(min(static_cast<int64_t>(TT), hi - t0 - TT)));
+        mbar_wait(&sm.y_full[yr.slot], yr.phase);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const int tg = tk + g * GK;
+          if (tg * 4 >= nt) break;
+          float4 even = make_float4(0.f, 0.f, 0.f, 0.f), odd = even;
+          const unsigned char* yp = &sm.y[yr.slot][tg][0][k0 / 2 * 16];
+#pragma unroll
+          for (int l = 0; l < L; ++l) {
+            const float4 a = *reinterpret_cast<const float4*>(yp + l * Sh::QS);
+            const float4 b = *reinterpret_cast<const float4*>(yp + l * Sh::QS + Sh::ODD);
+            even.x += a.x;
+            even.y += a.y;
+            even.z += a.z;
+            even.w += a.w;
+            odd.x += b.x;
+            odd.y += b.y;
+            odd.z += b.z;
+            odd.w += b.w;
+          }
+          const float ev[4] = {even.x, even.y, even.z, even.w}, od[4] = {odd.x, odd.y, odd.z, odd.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = tg * 4 + j, k = g * 4 + j;
+            if (t >= nt) break;
+            const float y[2] = {(ev[j] + du[k][0]) * gate[k][0], (od[j] + du[k][1]) * gate[k][1]};
+            T* to = out + (t0 + t) * p.o_st;
+            if ((p.wide & 32) && valid == 2) {
+              store_f32<T, 2>(to, y);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (i < valid) to[i] = from_f32<T>(y[i]);
+            }
+          }
+        }
+        mbar_arrive_warp(&sm.y_empty[yr.slot]);
+        yr.next();
+      }
+    });
   }
 }
 
 // ------------------------------------------------------------ single tokens
+constexpr int S = 4;  // states per thread of the kernels below
+
 struct DecodeParams {
   const void* u;
   const void* dt;
@@ -183,7 +496,7 @@ __global__ void __launch_bounds__(NTHREADS) ssm_decode_kernel(DecodeParams p) {
   if (live) {
     const int group = ch / (p.C / p.G);
     uu = to_f32(static_cast<const T*>(p.u)[r * p.u_st + ch]);
-    const float d = step_of(to_f32(static_cast<const T*>(p.dt)[r * p.dt_st + ch]) + (p.dt_bias ? p.dt_bias[ch] : 0.f),
+    const float d = step_of<sizeof(T) == 4>(to_f32(static_cast<const T*>(p.dt)[r * p.dt_st + ch]) + (p.dt_bias ? p.dt_bias[ch] : 0.f),
                             p.softplus);
     const T* bb = static_cast<const T*>(p.b) + r * p.b_st + group * p.b_sg;
     const T* cc = static_cast<const T*>(p.c) + r * p.c_st + group * p.c_sg;
@@ -225,10 +538,10 @@ struct BwdParams {
 
 template <int L>
 struct BwdShared {
-  float4 d[TT][NTHREADS / L];  // d, d u, dy (through the gate), u
-  float b[TT][L * S], c[TT][L * S];
-  float y[TT][NTHREADS / L], sum1[TT][NTHREADS / L], sum2[TT][NTHREADS / L];
-  float db[NTHREADS / 32][TT][L * S], dc[NTHREADS / 32][TT][L * S];  // each warp's
+  float4 d[KT][NTHREADS / L];  // d, d u, dy (through the gate), u
+  float b[KT][L * S], c[KT][L * S];
+  float y[KT][NTHREADS / L], sum1[KT][NTHREADS / L], sum2[KT][NTHREADS / L];
+  float db[NTHREADS / 32][KT][L * S], dc[NTHREADS / 32][KT][L * S];  // each warp's
 };
 
 // The sequence backwards, a tile at a time: from the state kept before the
@@ -240,15 +553,15 @@ __global__ void __launch_bounds__(NTHREADS) ssm_bwd_kernel(BwdParams bp) {
   const Params& p = bp.f;
   constexpr int CH = NTHREADS / L;
   extern __shared__ __align__(16) unsigned char smem[];
-  BwdShared<L>& sm = *reinterpret_cast<BwdShared<L>*>(smem);
-  auto& s_d = sm.d;
-  auto& s_b = sm.b;
-  auto& s_c = sm.c;
-  auto& s_y = sm.y;
-  auto& s_1 = sm.sum1;
-  auto& s_2 = sm.sum2;
-  auto& s_db = sm.db;
-  auto& s_dc = sm.dc;
+  BwdShared<L>& shm = *reinterpret_cast<BwdShared<L>*>(smem);
+  auto& s_d = shm.d;
+  auto& s_b = shm.b;
+  auto& s_c = shm.c;
+  auto& s_y = shm.y;
+  auto& s_1 = shm.sum1;
+  auto& s_2 = shm.sum2;
+  auto& s_db = shm.db;
+  auto& s_dc = shm.dc;
   constexpr int NP = L * S;
   const int tid = threadIdx.x, q = tid % L, ch = tid / L, warp = tid / 32, lane = tid % 32;
   const int seq = blockIdx.y;
@@ -271,17 +584,17 @@ __global__ void __launch_bounds__(NTHREADS) ssm_bwd_kernel(BwdParams bp) {
     g[i] = live && n < p.N && bp.dfin ? bp.dfin[static_cast<int64_t>(seq) * p.C * p.N + at] : 0.f;
   }
   float sum_d = 0.f, sum_bias = 0.f;  // thread tid < CH: channel c0 + tid
-  const int64_t tiles = (end - start + TT - 1) / TT;
+  const int64_t tiles = (end - start + KT - 1) / KT;
   for (int64_t k = tiles - 1; k >= 0; --k) {
-    const int64_t t0 = start + k * TT;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(TT), end - t0));
+    const int64_t t0 = start + k * KT;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(KT), end - t0));
     __syncthreads();
-    for (int i = tid; i < TT * CH; i += NTHREADS) {
+    for (int i = tid; i < KT * CH; i += NTHREADS) {
       const int t = i / CH, m = i % CH;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (t < nt && c0 + m < c_end) {
         const float r = to_f32(dt[(t0 + t) * p.dt_st + c0 + m]) + (p.dt_bias ? p.dt_bias[c0 + m] : 0.f);
-        v.x = step_of(r, p.softplus);
+        v.x = step_of<sizeof(T) == 4>(r, p.softplus);
         v.w = to_f32(u[(t0 + t) * p.u_st + c0 + m]);
         v.y = v.x * v.w;
         v.z = to_f32(dout[(t0 + t) * bp.dout_st + c0 + m]);
@@ -289,21 +602,21 @@ __global__ void __launch_bounds__(NTHREADS) ssm_bwd_kernel(BwdParams bp) {
       }
       s_d[t][m] = v;
     }
-    for (int i = tid; i < TT * NP; i += NTHREADS) {
+    for (int i = tid; i < KT * NP; i += NTHREADS) {
       const int t = i / NP, n = i % NP;
       const bool in = t < nt && n < p.N;
       s_b[t][n] = in ? to_f32(bb[(t0 + t) * p.b_st + n]) : 0.f;
       s_c[t][n] = in ? to_f32(cc[(t0 + t) * p.c_st + n]) : 0.f;
     }
     __syncthreads();
-    float h0[S], e[TT][S], h[TT][S];
+    float h0[S], e[KT][S], h[KT][S];
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       const int n = q * S + i;
-      h0[i] = live && n < p.N ? p.ck[((first_tile(start, seq) + k) * p.C + c0 + ch) * p.N + n] : 0.f;
+      h0[i] = live && n < p.N ? p.ck[((first_kept(start, seq) + k) * p.C + c0 + ch) * p.N + n] : 0.f;
     }
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {  // past the sequence's end d = 0: the state stays
+    for (int t = 0; t < KT; ++t) {  // past the sequence's end d = 0: the state stays
       const float4 d = s_d[t][ch];
       float y = 0.f;
 #pragma unroll
@@ -319,7 +632,7 @@ __global__ void __launch_bounds__(NTHREADS) ssm_bwd_kernel(BwdParams bp) {
       }
     }
 #pragma unroll
-    for (int t = TT - 1; t >= 0; --t) {
+    for (int t = KT - 1; t >= 0; --t) {
       const float4 d = s_d[t][ch];
       float s1 = 0.f, s2 = 0.f;
 #pragma unroll

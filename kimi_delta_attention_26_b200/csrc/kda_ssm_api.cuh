@@ -43,25 +43,6 @@ kda_status_t check_ssm(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_
   return KDA_OK;
 }
 
-// Threads per channel: each holds ssm::S of its states.
-template <typename F>
-void by_lanes(int64_t N, F f) {
-  const int64_t l = (N + kda::ssm::S - 1) / kda::ssm::S;
-  if (l <= 4) f(std::integral_constant<int, 4>());
-  else if (l <= 8) f(std::integral_constant<int, 8>());
-  else if (l <= 16) f(std::integral_constant<int, 16>());
-  else f(std::integral_constant<int, 32>());
-}
-
-template <typename F>
-void by_ssm(kda_dtype_t dt, int64_t N, F f) {
-  by_lanes(N, [&](auto l) {
-    if (dt == KDA_BF16) f(__nv_bfloat16(), l);
-    else if (dt == KDA_F16) f(__half(), l);
-    else f(float(), l);
-  });
-}
-
 kda::ssm::Params ssm_params(const SsmArgs& a, int32_t softplus, const int32_t* cu, int32_t num_seqs, const void* init) {
   kda::ssm::Params p;
   std::memset(&p, 0, sizeof(p));
@@ -88,6 +69,12 @@ kda::ssm::Params ssm_params(const SsmArgs& a, int32_t softplus, const int32_t* c
   p.N = static_cast<int>(a.N);
   p.G = static_cast<int>(a.G);
   p.softplus = softplus;
+  // two channels at a time: every block's and group's first channel is even
+  const int pair = 2 * io_bytes(a.dt), quad = 2 * pair;
+  const bool even = a.C / a.G % 2 == 0 || a.G == 1;
+  p.wide = (even && aligned(a.u, pair) ? 1 : 0) | (even && aligned(a.dt_, pair) ? 2 : 0) | (even && aligned(a.z, pair) ? 4 : 0) |
+           (a.N % 4 == 0 && aligned(a.b, quad) ? 8 : 0) | (a.N % 4 == 0 && aligned(a.c, quad) ? 16 : 0) |
+           (even && aligned(a.out, pair) ? 32 : 0);
   return p;
 }
 
@@ -122,14 +109,8 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.out = a.out.data;
   p.o_st = a.out.st;
   p.fin = static_cast<float*>(fin);
-  by_ssm(a.dt, a.N, [&](auto t, auto l) {
-    constexpr int CH = sm::NTHREADS / l.value;
-    p.blocks_per_group = static_cast<int>((a.C / a.G + CH - 1) / CH);
-    sm::ssm_fwd_kernel<decltype(t), l.value, true>
-        <<<dim3(static_cast<unsigned>(a.G * p.blocks_per_group), num_seqs), sm::NTHREADS, 0,
-           static_cast<cudaStream_t>(stream)>>>(p);
-  });
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      by_type(a.dt, [&](auto m) { return m.scan(p, true, num_seqs, g_num_sms[dev], static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
 
@@ -181,13 +162,7 @@ kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const
   p.N = static_cast<int>(a.N);
   p.G = static_cast<int>(a.G);
   p.softplus = dt_softplus != 0;
-  by_ssm(a.dt, a.N, [&](auto t, auto l) {
-    constexpr int CH = sm::NTHREADS / l.value;
-    sm::ssm_decode_kernel<decltype(t), l.value>
-        <<<dim3(static_cast<unsigned>(B_), static_cast<unsigned>((a.C + CH - 1) / CH)), sm::NTHREADS, 0,
-           static_cast<cudaStream_t>(stream)>>>(p);
-  });
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan_decode(p, B_, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
 
@@ -231,14 +206,11 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   sm::BwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.f = ssm_params(a, dt_softplus != 0, cu_seqlens, num_seqs, init);
-  int blocks = 0;
-  by_ssm(a.dt, a.N, [&](auto, auto l) {
-    constexpr int CH = sm::NTHREADS / l.value;
-    p.f.blocks_per_group = static_cast<int>((a.C / a.G + CH - 1) / CH);
-    blocks = static_cast<int>(a.G) * p.f.blocks_per_group;
-  });
+  const int ch = 128 / sm::threads_per_channel(static_cast<int>(a.N));
+  p.f.blocks_per_group = static_cast<int>((a.C / a.G + ch - 1) / ch);
+  const int blocks = static_cast<int>(a.G) * p.f.blocks_per_group;
   const size_t cn = static_cast<size_t>(a.C) * a.N;
-  const size_t ck_bytes = round256((static_cast<size_t>(a.T) / sm::TT + num_seqs) * cn * 4);
+  const size_t ck_bytes = round256((static_cast<size_t>(a.T) / sm::KT + num_seqs) * cn * 4);
   const size_t a_bytes = round256(num_seqs * cn * 4), d_bytes = round256(2 * static_cast<size_t>(num_seqs) * a.C * 4);
   const size_t b_bytes = round256(static_cast<size_t>(blocks) * a.T * a.N * 4);
   void* scratch = nullptr;
@@ -291,17 +263,11 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   const int64_t most = std::max<int64_t>(a.T * a.G * a.N, static_cast<int64_t>(cn));
   const unsigned reduce_blocks =
       static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 8 * static_cast<int64_t>(g_num_sms[dev])));
-  by_ssm(a.dt, a.N, [&](auto t, auto l) {
-    const dim3 grid(blocks, num_seqs);
-    sm::ssm_fwd_kernel<decltype(t), l.value, false><<<grid, sm::NTHREADS, 0, cs>>>(p.f);
-    constexpr size_t bytes = sizeof(sm::BwdShared<l.value>);
-    if (bytes > 48 * 1024)
-      cudaFuncSetAttribute(sm::ssm_bwd_kernel<decltype(t), l.value>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(bytes));
-    sm::ssm_bwd_kernel<decltype(t), l.value><<<grid, sm::NTHREADS, bytes, cs>>>(p);
+  e = by_type(a.dt, [&](auto m) {
+    cudaError_t f = m.scan(p.f, false, num_seqs, g_num_sms[dev], cs);
+    if (f == cudaSuccess) f = m.scan_bwd(p, cs);
+    return f == cudaSuccess ? m.scan_reduce(r, reduce_blocks, cs) : f;
   });
-  by_ssm(a.dt, 1, [&](auto t, auto) { sm::ssm_reduce_kernel<decltype(t)><<<reduce_blocks, 256, 0, cs>>>(r); });
-  e = cudaGetLastError();
   const cudaError_t ef = cudaFreeAsync(scratch, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   return ef != cudaSuccess ? cuda_fail(ef) : KDA_OK;
