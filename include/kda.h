@@ -359,8 +359,8 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  *     and T = 0 are allowed. Violations are recorded in the device status word.
  *   - An output may not overlap an input or another output (KDA_ERR_OVERLAP)
  *     unless the call says so.
- *   - Results are deterministic: no atomics on data. kda_conv_bwd and
- *     kda_ssm_bwd take scratch from the library's pool, the others none.
+ *   - Results are deterministic: no atomics on data. kda_conv_bwd, kda_ssm_bwd
+ *     and a time-split kda_ssm_fwd take scratch from the library's pool.
  *   - Calls can be captured into CUDA graphs and run on any stream.
  */
 #define KDA_ACT_NONE 0
@@ -419,6 +419,11 @@ kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
  *   D, dt_bias      fp32 [C] or NULL (zeros)
  *   initial_state   fp32 [N, C, S] or NULL (zeros)
  *   final_state     the same or NULL; may be initial_state itself
+ *
+ * Where there are few channels and sequences for the device's SMs, ranges of the
+ * packed tokens are scanned side by side (the time split; kda_set_time_split
+ * applies: 0 automatic, 1 never, 2 from 128 tokens on, for testing). Results
+ * then agree with the unsplit scan within rounding, not bitwise.
  */
 kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
                          const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,

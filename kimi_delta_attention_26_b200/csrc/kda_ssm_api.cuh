@@ -43,6 +43,26 @@ kda_status_t check_ssm(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_
   return KDA_OK;
 }
 
+// The time split of the forward scan: tokens per range, or 0. A range's blocks
+// run beside the other ranges'; a first pass over the pieces that go on in the
+// next range gives each range's start. Where one block per (sequence, channels)
+// leaves half of the SMs idle: as many ranges as fill two blocks per SM, of 256
+// tokens at least (the first pass costs about 3/4 of the second). Measured on
+// 32768 tokens x 1024 channels x 16 states (32 blocks): SPLIT_FIGURES
+int64_t scan_run(const SsmArgs& a, int32_t num_seqs, int64_t blocks, int dev) {
+  const int mode = g_split.load();
+  if (mode == 1) return 0;
+  if (mode == 2) return a.T >= 128 ? 64 : 0;  // testing
+  if (2 * blocks * num_seqs > g_num_sms[dev] || a.T < 1024) return 0;
+  const int64_t ranges = std::min<int64_t>(2 * g_num_sms[dev] / blocks, a.T / 256);
+  return ((a.T + ranges - 1) / ranges + 31) / 32 * 32;
+}
+
+int64_t scan_blocks(const SsmArgs& a) {
+  const int ch = 128 / kda::ssm::threads_per_channel(static_cast<int>(a.N));
+  return a.G * ((a.C / a.G + ch - 1) / ch);
+}
+
 kda::ssm::Params ssm_params(const SsmArgs& a, int32_t softplus, const int32_t* cu, int32_t num_seqs, const void* init) {
   kda::ssm::Params p;
   std::memset(&p, 0, sizeof(p));
@@ -109,9 +129,38 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.out = a.out.data;
   p.o_st = a.out.st;
   p.fin = static_cast<float*>(fin);
-  const cudaError_t e =
-      by_type(a.dt, [&](auto m) { return m.scan(p, true, num_seqs, g_num_sms[dev], static_cast<cudaStream_t>(stream)); });
-  return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int sms = g_num_sms[dev];
+  const int64_t run = scan_run(a, num_seqs, scan_blocks(a), dev);
+  if (!run) {
+    const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan(p, true, num_seqs, sms, cs); });
+    return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
+  }
+  if ((st = prepare_pool(dev)) != KDA_OK) return st;
+  const int ranges = static_cast<int>((a.T + run - 1) / run);
+  // A final state in the initial state's place is written behind the scan: its
+  // last range's block may end before the first range's has read the state.
+  const bool in_place = fin && fin == init;
+  const size_t state_bytes = static_cast<size_t>(num_seqs) * a.C * a.N * 4;
+  const size_t carry_bytes = round256(static_cast<size_t>(ranges) * a.C * a.N * 4);
+  const size_t sum_bytes = round256(static_cast<size_t>(ranges) * a.C * 4);
+  void* scratch = nullptr;
+  cudaError_t e =
+      cudaMallocFromPoolAsync(&scratch, carry_bytes + sum_bytes + (in_place ? state_bytes : 0), g_pool[dev].load(), cs);
+  if (e != cudaSuccess) return cuda_fail(e);
+  unsigned char* sb = static_cast<unsigned char*>(scratch);
+  p.run = run;
+  p.carry = reinterpret_cast<float*>(sb);
+  p.sum_d = reinterpret_cast<float*>(sb + carry_bytes);
+  if (in_place) p.fin = reinterpret_cast<float*>(sb + carry_bytes + sum_bytes);
+  e = by_type(a.dt, [&](auto m) {
+    const cudaError_t f = ranges > 1 ? m.scan(p, false, ranges - 1, sms, cs) : cudaSuccess;
+    return f == cudaSuccess ? m.scan(p, true, ranges, sms, cs) : f;
+  });
+  if (e == cudaSuccess && in_place) e = cudaMemcpyAsync(fin, p.fin, state_bytes, cudaMemcpyDeviceToDevice, cs);
+  const cudaError_t ef = cudaFreeAsync(scratch, cs);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return ef != cudaSuccess ? cuda_fail(ef) : KDA_OK;
 }
 
 kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
@@ -206,9 +255,8 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   sm::BwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.f = ssm_params(a, dt_softplus != 0, cu_seqlens, num_seqs, init);
-  const int ch = 128 / sm::threads_per_channel(static_cast<int>(a.N));
-  p.f.blocks_per_group = static_cast<int>((a.C / a.G + ch - 1) / ch);
-  const int blocks = static_cast<int>(a.G) * p.f.blocks_per_group;
+  const int64_t blocks = scan_blocks(a);
+  p.f.blocks_per_group = static_cast<int>(blocks / a.G);
   const size_t cn = static_cast<size_t>(a.C) * a.N;
   const size_t ck_bytes = round256((static_cast<size_t>(a.T) / sm::KT + num_seqs) * cn * 4);
   const size_t a_bytes = round256(num_seqs * cn * 4), d_bytes = round256(2 * static_cast<size_t>(num_seqs) * a.C * 4);

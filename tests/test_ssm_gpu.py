@@ -128,6 +128,57 @@ def test_scan_long(kda, typ):
     check_all(kda, make(lens, 48, 16, 1, TYPES[typ], seed=4), lens)
 
 
+@pytest.mark.parametrize("n,G,typ", [(16, 1, "bf16"), (5, 3, "f32"), (128, 1, "f16"), (30, 5, "f32")])
+@pytest.mark.parametrize("lens", [[128], [700], [64, 64, 64], [1, 0, 63, 200, 64, 0, 130, 0], [300, 5]],
+                         ids=lambda x: f"{len(x)}seq{sum(x)}")
+def test_scan_time_split(kda, lens, n, G, typ):
+    """Ranges of 64 tokens side by side: sequences that end and start at, before
+    and after the ranges' borders, sequences over several ranges, empty ones."""
+    d = make(lens, 45, n, G, TYPES[typ], gate=n != 5, state=n != 30, seed=n)
+    try:
+        kda.set_time_split(2)
+        check_all(kda, d, lens)
+        if d["init"] is not None:
+            cu, state = cu_of(lens), d["init"].clone()
+            _, ref = fwd(kda, d, cu, initial_state=d["init"])
+            _, fin = fwd(kda, d, cu, initial_state=state, final_state=state)
+            assert fin is state and torch.equal(state, ref)
+    finally:
+        kda.set_time_split(0)
+
+
+def test_scan_time_split_is_taken_by_itself(kda):
+    """One long sequence with few channels: the split's result agrees with the
+    reference, and is not bitwise the unsplit scan's (so it was taken)."""
+    d = make([2100], 64, 16, 1, torch.float32, seed=41)
+    check_all(kda, d, [2100])
+    a, _ = fwd(kda, d, initial_state=d["init"])
+    try:
+        kda.set_time_split(1)
+        b, _ = fwd(kda, d, initial_state=d["init"])
+    finally:
+        kda.set_time_split(0)
+    assert not torch.equal(a, b)
+
+
+def test_scan_time_split_padded_and_bad_boundaries(kda):
+    d = make([200], 40, 16, 1, torch.bfloat16, state=False, seed=43)
+    for k in ("u", "dt", "B", "C", "z"):
+        d[k][153:] = float("nan")
+    try:
+        kda.set_time_split(2)
+        out = torch.full((200, 40), 5.0, dtype=torch.bfloat16, device="cuda")
+        _, fin = fwd(kda, d, cu_of([100, 53]), out=out)
+        ref, rfin = fwd(kda, d, cu_of([100, 53]), rows=slice(0, 153))
+        assert torch.equal(out[:153], ref) and bool((out[153:] == 5).all()) and torch.equal(fin, rfin)
+        assert kda.device_status(reset=True) == 0
+        for bad in ([0, 150, 20, 200], [0, 130, 299, 10 ** 9], [-5, 10, 140, 200], [70, 80, 90, 200]):
+            fwd(kda, d, torch.tensor(bad, dtype=torch.int32, device="cuda"))
+            assert kda.device_status(reset=True) == 1, bad
+    finally:
+        kda.set_time_split(0)
+
+
 def test_scan_many_channels(kda):
     lens = [60, 90]
     check_all(kda, make(lens, 1000, 16, 1, torch.bfloat16, seed=6), lens)
