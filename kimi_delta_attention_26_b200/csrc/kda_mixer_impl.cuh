@@ -109,9 +109,7 @@ template <typename T>
 cudaError_t Mixer<T>::scan_bwd(ssm::BwdParams p, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   by_states(p.f.N, [&](auto l, auto) {
-    constexpr int CH = ssm::NTHREADS / l.value;
     constexpr size_t bytes = sizeof(ssm::BwdShared<l.value>);
-    p.f.blocks_per_group = (p.f.C / p.f.G + CH - 1) / CH;
     auto* kernel = ssm::ssm_bwd_kernel<T, l.value>;
     if ((e = allow_shared(kernel, bytes)) == cudaSuccess)
       kernel<<<dim3(p.f.G * p.f.blocks_per_group, p.f.NS), ssm::NTHREADS, bytes, stream>>>(p);

@@ -254,9 +254,13 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   sm::BwdParams p;
   std::memset(&p, 0, sizeof(p));
+  const int pair = 2 * io_bytes(a.dt);
+  const bool even = a.C / a.G % 2 == 0 || a.G == 1;
   p.f = ssm_params(a, dt_softplus != 0, cu_seqlens, num_seqs, init);
-  const int64_t blocks = scan_blocks(a);
-  p.f.blocks_per_group = static_cast<int>(blocks / a.G);
+  // blocks of the gradients' kernel: 256 / (threads per channel) channels each
+  const int ch = 256 / sm::threads_per_channel(static_cast<int>(a.N));
+  p.f.blocks_per_group = static_cast<int>((a.C / a.G + ch - 1) / ch);
+  const int64_t blocks = a.G * p.f.blocks_per_group;
   const size_t cn = static_cast<size_t>(a.C) * a.N;
   const size_t ck_bytes = round256((static_cast<size_t>(a.T) / sm::KT + num_seqs) * cn * 4);
   const size_t a_bytes = round256(num_seqs * cn * 4), d_bytes = round256(2 * static_cast<size_t>(num_seqs) * a.C * 4);
@@ -280,6 +284,7 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.ddt_st = vddt.st;
   p.dz_st = vdz.st;
   p.dinit = static_cast<float*>(dinit);
+  p.wide = (even && aligned(vddt, pair) ? 1 : 0) | (even && aligned(vdu, pair) ? 2 : 0) | (even && aligned(vdz, pair) ? 4 : 0);
   sm::ReduceParams r;
   std::memset(&r, 0, sizeof(r));
   r.part_a = p.part_a;
