@@ -112,7 +112,7 @@ cudaError_t Mixer<T>::scan_bwd(ssm::BwdParams p, cudaStream_t stream) {
     constexpr size_t bytes = sizeof(ssm::BwdShared<l.value>);
     auto* kernel = ssm::ssm_bwd_kernel<T, l.value>;
     if ((e = allow_shared(kernel, bytes)) == cudaSuccess)
-      kernel<<<dim3(p.f.G * p.f.blocks_per_group, p.f.NS), ssm::NTHREADS, bytes, stream>>>(p);
+      kernel<<<dim3(p.f.G * p.f.blocks_per_group, p.f.NS), ssm::BwdShared<l.value>::THREADS, bytes, stream>>>(p);
   });
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -20,6 +20,9 @@ constexpr int YSLOTS = 2;      // tiles of outputs in flight
 
 // Threads that share a channel's N states, four each.
 inline int threads_per_channel(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+// Channels of a block of the forward scan and of its gradients.
+inline int scan_channels(int N) { return 128 / threads_per_channel(N); }
+inline int bwd_channels(int N) { return (N <= 32 ? 256 : 128) / threads_per_channel(N); }
 
 struct Params {
   const void* u;
@@ -534,32 +537,32 @@ struct BwdParams {
   float* part_b;            // [channel blocks, T, N]
   float* part_c;
   int64_t dout_st, du_st, ddt_st, dz_st;
-  int wide;                 // bits 0..2: rows of ddt, du, dz can be written two channels at a time
 };
 
 constexpr int TB = 16;  // tokens per tile of the gradients, in two halves of KT
 
-// The gradients' block: four warps of 32 / L lanes of channel pairs, L threads
-// of four states per pair of channels.
+// The gradients' block: WARPS warps of 32 / L channels, L threads of four states
+// per channel.
 template <int L>
 struct BwdShared {
-  static constexpr int CH = 4 * 64 / L;                      // channels
+  static constexpr int WARPS = L <= 8 ? 8 : 4, THREADS = 32 * WARPS;
+  static constexpr int CH = WARPS * 32 / L;                  // channels
   static constexpr int FB = L <= 8 ? 4 : L == 16 ? 2 : 1;    // orders of B and C, see the kernel
-  static constexpr int ODD = CH / 2 * 16, QS = 2 * ODD + 32;  // rows of the parts of sums, by state group
-  float4 d[TB][CH / 2];        // d, d u of both channels of a pair
-  float2 dy[TB][CH / 2];       // the output's gradient, through the gate
+  // parts of sums, 16 bytes (four tokens) per thread, even channels before odd
+  // ones; the strides put the threads of a store and of a load into different banks
+  static constexpr int ODD = CH / 2 * 16 + 64, QS = 2 * ODD + 16;
+  float2 d[TB][CH];            // d, d u
+  float dy[TB][CH];            // the output's gradient, through the gate
   float2 u[TB][CH / 2], sig[TB][CH / 2], zf[TB][CH / 2];  // u; softplus'; dout times the gate's slope
   alignas(16) float b[TB][FB][4 * L], c[TB][FB][4 * L];
-  alignas(16) unsigned char sum[3][TB / 4][L][QS];  // sum_n g B, sum_n q A, sum_n C h by threads: four tokens each
-  float db[4][TB][4 * L], dc[4][TB][4 * L];  // each warp's
+  alignas(16) unsigned char sum[3][TB / 4][L][QS];  // sum_n g B, sum_n w A, sum_n C h by threads
+  float db[WARPS][TB][4 * L], dc[WARPS][TB][4 * L];
 };
 
 // The sequence backwards, a tile at a time: from the kept states its states and
 // decays again, KT tokens in registers, then the reverse recurrence
 //   g_t = dy_t C_t + a_{t+1} g_{t+1},  w_t = a_t g_t h_{t-1}
 //   dC += dy h,  dB += g d u,  dd = sum_n w A + u sum_n g B,  du = d sum_n g B + D dy,  dA += d w
-// A thread has two channels, so that their dB and dC are one sum and B and C are
-// read once for both.
 //
 // dB and dC are sums over channels, that is over lanes. A lane's register i holds
 // state i ^ f of its four, f from two of the lane's channel bits: then the lanes
@@ -567,101 +570,104 @@ struct BwdShared {
 // keep the others, two exchanges and one instead of four a step, without
 // selecting by lane. B and C stand in shared memory in each order.
 template <typename T, int L>
-__global__ void __launch_bounds__(NTHREADS, L <= 8 ? 2 : 1) ssm_bwd_kernel(BwdParams bp) {
+__global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd_kernel(BwdParams bp) {
   using Sh = BwdShared<L>;
   const Params& p = bp.f;
-  constexpr int CH = Sh::CH, FB = Sh::FB;
+  constexpr int CH = Sh::CH, FB = Sh::FB, NT = Sh::THREADS, NP = 4 * L;
   constexpr unsigned ALL = 0xffffffffu;
   extern __shared__ __align__(16) unsigned char smem[];
   Sh& sm = *reinterpret_cast<Sh*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // lane bits of the thread's state group q, its pair of channels and its order f
+  // lane bits of the thread's state group q, its channel and its order f
   const int b1 = lane >> 1 & 1, hi = lane >> 3, rest = (lane & 1) | (lane >> 2 << 1);
   const int q = L == 32 ? lane : rest % L;
-  const int pair = warp * (32 / L) + (L == 32 ? 0 : L == 4 ? b1 | hi << 1 : b1 | rest / L << 1);
+  const int chl = warp * (32 / L) + (L == 32 ? 0 : L == 4 ? b1 | hi << 1 : b1 | rest / L << 1);
   const int f = L == 4 ? hi : L == 8 ? b1 | (lane >> 4) << 1 : L == 16 ? b1 : 0;
   const int seq = blockIdx.y;
   const int group = blockIdx.x / p.blocks_per_group, cg = p.C / p.G;
   const int c0 = group * cg + (blockIdx.x % p.blocks_per_group) * CH, c_end = min(c0 + CH, (group + 1) * cg);
   const int64_t start = bound(p.cu, seq, p.T), end = max(start, bound(p.cu, seq + 1, p.T));
   const int64_t cn = static_cast<int64_t>(p.C) * p.N;
-  float a[2][4], g[2][4], da[2][4];
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
+  const int ch = c0 + chl;
+  const bool live = ch < c_end;
+  float2 a[2], g[2], da[2];
+  {
+    float av[4], gv[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int n = q * 4 + (i ^ f), ch = c0 + 2 * pair + c;
-      const bool on = ch < c_end && n < p.N;
+      const int n = q * 4 + (i ^ f);
+      const bool on = live && n < p.N;
       const int64_t at = static_cast<int64_t>(ch) * p.N + n;
-      a[c][i] = on ? p.A[at] * kLog2e : 0.f;
-      g[c][i] = on && bp.dfin ? bp.dfin[seq * cn + at] : 0.f;
-      da[c][i] = 0.f;
+      av[i] = on ? p.A[at] * kLog2e : 0.f;
+      gv[i] = on && bp.dfin ? bp.dfin[seq * cn + at] : 0.f;
     }
-  // this thread's part of a tile before and after the states: a channel pair's
-  // four tokens (of every GK-th four)
-  constexpr int PAIRS = CH / 2, GK = NTHREADS / PAIRS, NG = (TB / 4 + GK - 1) / GK;
-  const int mp = tid % PAIRS, mg = tid / PAIRS, mc = c0 + 2 * mp, valid = max(0, min(2, c_end - mc));
-  float bias[2], skip[2], sum_d[2] = {0.f, 0.f}, sum_bias[2] = {0.f, 0.f};
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    bias[c] = p.dt_bias && c < valid ? p.dt_bias[mc + c] : 0.f;
-    skip[c] = p.D && c < valid ? p.D[mc + c] : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      a[i] = make_float2(av[2 * i], av[2 * i + 1]);
+      g[i] = make_float2(gv[2 * i], gv[2 * i + 1]);
+      da[i] = make_float2(0.f, 0.f);
+    }
   }
-  const T* u = static_cast<const T*>(p.u) + mc;
-  const T* dt = static_cast<const T*>(p.dt) + mc;
-  const T* z = static_cast<const T*>(p.z) + mc;
-  const T* dout = static_cast<const T*>(bp.dout) + mc;
-  const T* bb = static_cast<const T*>(p.b) + group * p.b_sg;
-  const T* cc = static_cast<const T*>(p.c) + group * p.c_sg;
+  unsigned char* const sum_row = &sm.sum[0][0][q][chl % 2 * Sh::ODD + chl / 2 * 16];
+  constexpr int SUM = TB / 4 * L * Sh::QS;  // bytes between the kinds of sums
+  // this thread's part of a tile before and after the states: a channel pair's TG tokens
+  constexpr int PAIRS = CH / 2, TG = TB * PAIRS / NT > 0 ? TB * PAIRS / NT : 1;
+  const int mp = tid % PAIRS, m0 = tid / PAIRS * TG, mc = c0 + 2 * mp, valid = max(0, min(2, c_end - mc));
+  float bias[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) bias[c] = p.dt_bias && c < valid ? p.dt_bias[mc + c] : 0.f;
+  // and after them: a channel's four tokens from xt on
+  const int xc = tid % CH, xt = tid / CH * 4;
+  const float skip = p.D && c0 + xc < c_end ? p.D[c0 + xc] : 0.f;
+  float sum_d = 0.f, sum_bias = 0.f;
   const int64_t tiles = (end - start + TB - 1) / TB;
   for (int64_t k = tiles - 1; k >= 0; --k) {
     const int64_t t0 = start + k * TB;
     const int nt = static_cast<int>(min(static_cast<int64_t>(TB), end - t0));
     // ------------------------------------------------ the tile's operands
+    if (m0 < TB) {
+      Vec<T, 2> vu[TG], vd[TG], vz[TG], vo[TG];
+      auto tok = [&](int j) { return t0 + min(m0 + j, nt - 1); };
+      load_rows(vd, static_cast<const T*>(p.dt) + mc, p.dt_st, valid, (p.wide & 2) && valid == 2, tok);
+      load_rows(vu, static_cast<const T*>(p.u) + mc, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
+      load_rows(vo, static_cast<const T*>(bp.dout) + mc, bp.dout_st, valid, (p.wide & 32) && valid == 2, tok);
+      if (p.z) load_rows(vz, static_cast<const T*>(p.z) + mc, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int tg = mg + i * GK;
-      if (TB / 4 % GK != 0 && tg >= TB / 4) break;
-      Vec<T, 2> vu[4], vd[4], vz[4], vo[4];
-      auto tok = [&](int j) { return t0 + min(tg * 4 + j, nt - 1); };
-      load_rows(vd, dt, p.dt_st, valid, (p.wide & 2) && valid == 2, tok);
-      load_rows(vu, u, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
-      load_rows(vo, dout, bp.dout_st, valid, (p.wide & 32) && valid == 2, tok);
-      if (p.z) load_rows(vz, z, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = tg * 4 + j;
+      for (int j = 0; j < TG; ++j) {
+        const int t = m0 + j;
         float d[2], du[2], dy[2], uu[2], sg[2], zf[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const float r = vd[j].get(c) + bias[c];
-          const bool on = t < nt && c < valid;  // else zeros: the state stays, nothing is added
-          uu[c] = on ? vu[j].get(c) : 0.f;
-          d[c] = on ? step_of<sizeof(T) == 4>(r, p.softplus) : 0.f;
-          du[c] = d[c] * uu[c];
+          d[c] = step_of<sizeof(T) == 4>(r, p.softplus);
           sg[c] = p.softplus ? sigmoid(r) : 1.f;
-          dy[c] = on ? vo[j].get(c) : 0.f;
+          uu[c] = vu[j].get(c);
+          dy[c] = vo[j].get(c);
           zf[c] = 0.f;
           if (p.z) {
             const float zz = vz[j].get(c), s = sigmoid(zz);
-            zf[c] = on ? dy[c] * s * fmaf(zz, 1.f - s, 1.f) : 0.f;
-            dy[c] *= on ? zz * s : 0.f;
+            zf[c] = dy[c] * s * fmaf(zz, 1.f - s, 1.f);
+            dy[c] *= zz * s;
           }
+          du[c] = d[c] * uu[c];
+          if (t >= nt || c >= valid) d[c] = du[c] = dy[c] = uu[c] = 0.f;  // the state stays, nothing is added
         }
-        sm.d[t][mp] = make_float4(d[0], du[0], d[1], du[1]);
-        sm.dy[t][mp] = make_float2(dy[0], dy[1]);
+        *reinterpret_cast<float4*>(&sm.d[t][2 * mp]) = make_float4(d[0], du[0], d[1], du[1]);
+        *reinterpret_cast<float2*>(&sm.dy[t][2 * mp]) = make_float2(dy[0], dy[1]);
         sm.u[t][mp] = make_float2(uu[0], uu[1]);
         sm.sig[t][mp] = make_float2(sg[0], sg[1]);
         if (p.z) sm.zf[t][mp] = make_float2(zf[0], zf[1]);
       }
     }
 #pragma unroll
-    for (int i = tid; i < TB * L; i += NTHREADS) {
+    for (int i = tid; i < TB * L; i += NT) {
       const int t = i / L, n0 = i % L * 4, nv = t < nt ? max(0, min(4, p.N - n0)) : 0;
       const int64_t tt = t0 + min(t, nt - 1);
       Vec<T, 4> vb[1], vc[1];
-      load_rows(vb, bb + n0, p.b_st, nv, (p.wide & 8) && nv == 4, [&](int) { return tt; });
-      load_rows(vc, cc + n0, p.c_st, nv, (p.wide & 16) && nv == 4, [&](int) { return tt; });
+      load_rows(vb, static_cast<const T*>(p.b) + group * p.b_sg + n0, p.b_st, nv, (p.wide & 8) && nv == 4,
+                [&](int) { return tt; });
+      load_rows(vc, static_cast<const T*>(p.c) + group * p.c_sg + n0, p.c_st, nv, (p.wide & 16) && nv == 4,
+                [&](int) { return tt; });
       float fb[4], fc[4];
       vb[0].get(fb);
       vc[0].get(fc);
@@ -673,107 +679,81 @@ __global__ void __launch_bounds__(NTHREADS, L <= 8 ? 2 : 1) ssm_bwd_kernel(BwdPa
     }
     __syncthreads();
     // -------------------------------------------------------- the states
-    float da_tile[2][4] = {};  // summed by tile: fewer roundings than token by token into one sum
+    float2 da_tile[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // by tile: fewer roundings than one long sum
+#pragma unroll 1
     for (int half = 1; half >= 0; --half) {
       if (half * KT >= nt) continue;
-      float2 h0[2][2], e[KT][2][2], h[KT][2][2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int ch = c0 + 2 * pair + c;
+      float2 h0[2], e[KT][2], h[KT][2];
+      {
         const int64_t at = ((first_kept(start, seq) + k * (TB / KT) + half) * p.C + ch) * p.N + q * 4;
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = 0.f;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (p.N % 4 == 0) {
-          if (ch < c_end && q * 4 < p.N) load_f32<float, 4>(v, p.ck + at);
+          if (live && q * 4 < p.N) load_f32<float, 4>(v, p.ck + at);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (ch < c_end && q * 4 + i < p.N) v[i] = p.ck[at + i];
+            if (live && q * 4 + i < p.N) v[i] = p.ck[at + i];
         }
         // into the lane's order
         const bool f0 = f & 1, f1 = f & 2;
         const float w0 = f0 ? v[1] : v[0], w1 = f0 ? v[0] : v[1], w2 = f0 ? v[3] : v[2], w3 = f0 ? v[2] : v[3];
-        h0[c][0] = f1 ? make_float2(w2, w3) : make_float2(w0, w1);
-        h0[c][1] = f1 ? make_float2(w0, w1) : make_float2(w2, w3);
+        h0[0] = f1 ? make_float2(w2, w3) : make_float2(w0, w1);
+        h0[1] = f1 ? make_float2(w0, w1) : make_float2(w2, w3);
       }
-      float y[2][4];
+      const float2* const dp = &sm.d[half * KT][chl];
+      const float* const yp = &sm.dy[half * KT][chl];
+      const float* const bq = &sm.b[half * KT][f][q * 4];
+      const float* const cq = &sm.c[half * KT][f][q * 4];
+      unsigned char* const sr = sum_row + half * (KT / 4) * (L * Sh::QS);
+      float y[4];
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
-        const int at = half * KT + t;
-        const float4 d = sm.d[at][pair];
-        const float4 b4 = *reinterpret_cast<const float4*>(&sm.b[at][f][q * 4]);
+        const float2 d = dp[t * CH];
+        const float4 b4 = *reinterpret_cast<const float4*>(bq + t * FB * NP);
         const float2 b[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+        const float2 dd = make_float2(d.x, d.x), du = make_float2(d.y, d.y);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float2 dd = c ? make_float2(d.z, d.z) : make_float2(d.x, d.x);
-          const float2 du = c ? make_float2(d.w, d.w) : make_float2(d.y, d.y);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            e[t][c][i] = pexp2(__fmul2_rn(dd, make_float2(a[c][2 * i], a[c][2 * i + 1])));
-            h[t][c][i] = __ffma2_rn(e[t][c][i], t ? h[t - 1][c][i] : h0[c][i], __fmul2_rn(du, b[i]));
-          }
+        for (int i = 0; i < 2; ++i) {
+          e[t][i] = pexp2(__fmul2_rn(dd, a[i]));
+          h[t][i] = __ffma2_rn(e[t][i], t ? h[t - 1][i] : h0[i], __fmul2_rn(du, b[i]));
         }
         if (p.z) {
-          const float4 c4 = *reinterpret_cast<const float4*>(&sm.c[at][f][q * 4]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float2 s = __ffma2_rn(make_float2(c4.z, c4.w), h[t][c][1], __fmul2_rn(make_float2(c4.x, c4.y), h[t][c][0]));
-            y[c][t % 4] = s.x + s.y;
-          }
-          if (t % 4 == 3) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              *reinterpret_cast<float4*>(&sm.sum[2][at / 4][q][c * Sh::ODD + pair * 16]) =
-                  make_float4(y[c][0], y[c][1], y[c][2], y[c][3]);
-          }
+          const float4 c4 = *reinterpret_cast<const float4*>(cq + t * FB * NP);
+          const float2 s = __ffma2_rn(make_float2(c4.z, c4.w), h[t][1], __fmul2_rn(make_float2(c4.x, c4.y), h[t][0]));
+          y[t % 4] = s.x + s.y;
+          if (t % 4 == 3)
+            *reinterpret_cast<float4*>(sr + 2 * SUM + t / 4 * (L * Sh::QS)) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
-      float s1[2][4], s2[2][4];
+      float s1[4], s2[4];
       float hold_b = 0.f, hold_c = 0.f;
 #pragma unroll
       for (int t = KT - 1; t >= 0; --t) {
         const int at = half * KT + t;
-        const float4 d = sm.d[at][pair];
-        const float2 dy = sm.dy[at][pair];
-        const float4 b4 = *reinterpret_cast<const float4*>(&sm.b[at][f][q * 4]);
-        const float4 c4 = *reinterpret_cast<const float4*>(&sm.c[at][f][q * 4]);
+        const float2 d = dp[t * CH];
+        const float yy = yp[t * CH];
+        const float4 b4 = *reinterpret_cast<const float4*>(bq + t * FB * NP);
+        const float4 c4 = *reinterpret_cast<const float4*>(cq + t * FB * NP);
         const float2 b[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
         const float2 cv[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
-        float2 vb[2], vc[2];
+        const float2 dd = make_float2(d.x, d.x), du = make_float2(d.y, d.y), y2 = make_float2(yy, yy);
+        float2 vb[2], vc[2], p1, p2;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float2 dd = c ? make_float2(d.z, d.z) : make_float2(d.x, d.x);
-          const float2 du = c ? make_float2(d.w, d.w) : make_float2(d.y, d.y);
-          const float2 y2 = c ? make_float2(dy.y, dy.y) : make_float2(dy.x, dy.x);
-          float2 p1, p2;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 gg = __ffma2_rn(y2, cv[i], make_float2(g[c][2 * i], g[c][2 * i + 1]));
-            vc[i] = c ? __ffma2_rn(y2, h[t][c][i], vc[i]) : __fmul2_rn(y2, h[t][c][i]);
-            vb[i] = c ? __ffma2_rn(du, gg, vb[i]) : __fmul2_rn(du, gg);
-            p1 = i ? __ffma2_rn(gg, b[i], p1) : __fmul2_rn(gg, b[i]);
-            const float2 ga = __fmul2_rn(gg, e[t][c][i]);
-            const float2 w = __fmul2_rn(ga, t ? h[t - 1][c][i] : h0[c][i]);
-            const float2 aa = make_float2(a[c][2 * i], a[c][2 * i + 1]);
-            p2 = i ? __ffma2_rn(w, aa, p2) : __fmul2_rn(w, aa);
-            const float2 s = __ffma2_rn(w, dd, make_float2(da_tile[c][2 * i], da_tile[c][2 * i + 1]));
-            da_tile[c][2 * i] = s.x;
-            da_tile[c][2 * i + 1] = s.y;
-            g[c][2 * i] = ga.x;
-            g[c][2 * i + 1] = ga.y;
-          }
-          s1[c][t % 4] = p1.x + p1.y;
-          s2[c][t % 4] = p2.x + p2.y;
+        for (int i = 0; i < 2; ++i) {
+          const float2 gg = __ffma2_rn(y2, cv[i], g[i]);
+          vc[i] = __fmul2_rn(y2, h[t][i]);
+          vb[i] = __fmul2_rn(du, gg);
+          p1 = i ? __ffma2_rn(gg, b[i], p1) : __fmul2_rn(gg, b[i]);
+          g[i] = __fmul2_rn(gg, e[t][i]);
+          const float2 w = __fmul2_rn(g[i], t ? h[t - 1][i] : h0[i]);
+          p2 = i ? __ffma2_rn(w, a[i], p2) : __fmul2_rn(w, a[i]);
+          da_tile[i] = __ffma2_rn(w, dd, da_tile[i]);
         }
+        s1[t % 4] = p1.x + p1.y;
+        s2[t % 4] = p2.x + p2.y;
         if (t % 4 == 0) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            *reinterpret_cast<float4*>(&sm.sum[0][at / 4][q][c * Sh::ODD + pair * 16]) =
-                make_float4(s1[c][0], s1[c][1], s1[c][2], s1[c][3]);
-            *reinterpret_cast<float4*>(&sm.sum[1][at / 4][q][c * Sh::ODD + pair * 16]) =
-                make_float4(s2[c][0], s2[c][1], s2[c][2], s2[c][3]);
-          }
+          *reinterpret_cast<float4*>(sr + t / 4 * (L * Sh::QS)) = make_float4(s1[0], s1[1], s1[2], s1[3]);
+          *reinterpret_cast<float4*>(sr + SUM + t / 4 * (L * Sh::QS)) = make_float4(s2[0], s2[1], s2[2], s2[3]);
         }
         // dB and dC over the warp's channels
         if constexpr (L <= 8) {
@@ -810,16 +790,18 @@ __global__ void __launch_bounds__(NTHREADS, L <= 8 ? 2 : 1) ssm_bwd_kernel(BwdPa
       }
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) da[c][i] += da_tile[c][i];
+    for (int i = 0; i < 2; ++i) {
+      da[i].x += da_tile[i].x;
+      da[i].y += da_tile[i].y;
+    }
     __syncthreads();
     // ------------------------------------------------------- the gradients
-    for (int i = tid; i < nt * p.N; i += NTHREADS) {
-      const int t = i / p.N, n = i % p.N;
+    for (int i = tid; i < nt * NP; i += NT) {
+      const int t = i / NP, n = i % NP;
+      if (n >= p.N) continue;
       float vb = 0.f, vc = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < Sh::WARPS; ++w) {
         vb += sm.db[w][t][n];
         vc += sm.dc[w][t][n];
       }
@@ -827,87 +809,62 @@ __global__ void __launch_bounds__(NTHREADS, L <= 8 ? 2 : 1) ssm_bwd_kernel(BwdPa
       bp.part_b[at] = vb;
       bp.part_c[at] = vc;
     }
-#pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int tg = mg + i * GK;
-      if (tg * 4 >= nt) break;
-      float s[3][2][4] = {};
+    if (xt < nt) {
+      float s[3][4] = {};
 #pragma unroll
       for (int m = 0; m < 3; ++m) {
         if (m == 2 && !p.z) break;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int l = 0; l < L; ++l) {
-            const float4 v = *reinterpret_cast<const float4*>(&sm.sum[m][tg][l][c * Sh::ODD + mp * 16]);
-            s[m][c][0] += v.x;
-            s[m][c][1] += v.y;
-            s[m][c][2] += v.z;
-            s[m][c][3] += v.w;
-          }
+        for (int l = 0; l < L; ++l) {
+          const float4 v = *reinterpret_cast<const float4*>(&sm.sum[m][xt / 4][l][xc % 2 * Sh::ODD + xc / 2 * 16]);
+          s[m][0] += v.x;
+          s[m][1] += v.y;
+          s[m][2] += v.z;
+          s[m][3] += v.w;
+        }
       }
+      const int64_t row = t0 + xt;
+      T* gd = static_cast<T*>(bp.ddt) + row * bp.ddt_st + c0 + xc;
+      T* gu = static_cast<T*>(bp.du) + row * bp.du_st + c0 + xc;
+      T* gz = static_cast<T*>(bp.dz) + row * bp.dz_st + c0 + xc;
 #pragma unroll
       for (int j = 3; j >= 0; --j) {
-        const int t = tg * 4 + j;
-        if (t >= nt) continue;
-        const float4 d4 = sm.d[t][mp];
-        const float2 dy2 = sm.dy[t][mp], u2 = sm.u[t][mp], sg2 = sm.sig[t][mp];
-        const float d[2] = {d4.x, d4.z}, dy[2] = {dy2.x, dy2.y}, uu[2] = {u2.x, u2.y}, sg[2] = {sg2.x, sg2.y};
-        float gd[2], gu[2], gz[2];
-        const float2 zf2 = p.z ? sm.zf[t][mp] : make_float2(0.f, 0.f);
-        const float zf[2] = {zf2.x, zf2.y};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          gd[c] = sg[c] * fmaf(uu[c], s[0][c][j], s[1][c][j] * 0.6931471805599453f);  // A came times log2(e)
-          gu[c] = fmaf(d[c], s[0][c][j], skip[c] * dy[c]);
-          gz[c] = zf[c] * fmaf(skip[c], uu[c], s[2][c][j]);
-          sum_bias[c] += gd[c];
-          sum_d[c] = fmaf(dy[c], uu[c], sum_d[c]);
-        }
-        auto put = [&](void* to, int64_t st, const float (&v)[2], int bit) {
-          T* row = static_cast<T*>(to) + (t0 + t) * st + mc;
-          if ((bp.wide & bit) && valid == 2) {
-            store_f32<T, 2>(row, v);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              if (c < valid) row[c] = from_f32<T>(v[c]);
-          }
-        };
-        put(bp.ddt, bp.ddt_st, gd, 1);
-        put(bp.du, bp.du_st, gu, 2);
-        if (p.z) put(bp.dz, bp.dz_st, gz, 4);
+        const int t = xt + j;
+        if (t >= nt || c0 + xc >= c_end) continue;
+        const float2 d = sm.d[t][xc];
+        const float dy = sm.dy[t][xc], uu = (&sm.u[t][0].x)[xc];
+        const float dd = (&sm.sig[t][0].x)[xc] * fmaf(uu, s[0][j], s[1][j] * 0.6931471805599453f);  // A came times log2(e)
+        sum_bias += dd;
+        sum_d = fmaf(dy, uu, sum_d);
+        gd[j * bp.ddt_st] = from_f32<T>(dd);
+        gu[j * bp.du_st] = from_f32<T>(fmaf(d.x, s[0][j], skip * dy));
+        if (p.z) gz[j * bp.dz_st] = from_f32<T>((&sm.zf[t][0].x)[xc] * fmaf(skip, uu, s[2][j]));
       }
     }
     __syncthreads();
   }
+  const float dv[4] = {da[0].x, da[0].y, da[1].x, da[1].y}, gv[4] = {g[0].x, g[0].y, g[1].x, g[1].y};
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = q * 4 + (i ^ f), ch = c0 + 2 * pair + c;
-      if (ch >= c_end || n >= p.N) continue;
-      const int64_t at = seq * cn + static_cast<int64_t>(ch) * p.N + n;
-      bp.part_a[at] = da[c][i];
-      if (bp.dinit) bp.dinit[at] = g[c][i];
-    }
-  // dD and ddt_bias: over the threads of a channel pair
-  float4* sums = reinterpret_cast<float4*>(&sm.d[0][0]);
-  sums[mg * PAIRS + mp] = make_float4(sum_d[0], sum_d[1], sum_bias[0], sum_bias[1]);
+  for (int i = 0; i < 4; ++i) {
+    const int n = q * 4 + (i ^ f);
+    if (!live || n >= p.N) continue;
+    const int64_t at = seq * cn + static_cast<int64_t>(ch) * p.N + n;
+    bp.part_a[at] = dv[i];
+    if (bp.dinit) bp.dinit[at] = gv[i];
+  }
+  // dD and ddt_bias: over the threads of a channel
+  float2* sums = reinterpret_cast<float2*>(sm.sum);
+  static_assert(sizeof(float2) * NT <= sizeof(sm.sum), "");
+  sums[tid] = make_float2(sum_d, sum_bias);
   __syncthreads();
-  if (mg == 0) {
-    float4 v = sums[mp];
-    for (int i = 1; i < GK; ++i) {
-      const float4 w = sums[i * PAIRS + mp];
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
+  if (tid < CH && c0 + tid < c_end) {
+    float2 v = sums[tid];
+    for (int i = tid + CH; i < NT; i += CH) {
+      v.x += sums[i].x;
+      v.y += sums[i].y;
     }
-    float* pd = bp.part_d + static_cast<int64_t>(seq) * p.C + mc;
-    float* pb = pd + static_cast<int64_t>(p.NS) * p.C;
-    if (valid > 0) pd[0] = v.x, pb[0] = v.z;
-    if (valid > 1) pd[1] = v.y, pb[1] = v.w;
+    bp.part_d[static_cast<int64_t>(seq) * p.C + c0 + tid] = v.x;
+    bp.part_d[(static_cast<int64_t>(p.NS) + seq) * p.C + c0 + tid] = v.y;
   }
 }
 

@@ -59,7 +59,7 @@ int64_t scan_run(const SsmArgs& a, int32_t num_seqs, int64_t blocks, int dev) {
 }
 
 int64_t scan_blocks(const SsmArgs& a) {
-  const int ch = 128 / kda::ssm::threads_per_channel(static_cast<int>(a.N));
+  const int ch = kda::ssm::scan_channels(static_cast<int>(a.N));
   return a.G * ((a.C / a.G + ch - 1) / ch);
 }
 
@@ -254,11 +254,8 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   sm::BwdParams p;
   std::memset(&p, 0, sizeof(p));
-  const int pair = 2 * io_bytes(a.dt);
-  const bool even = a.C / a.G % 2 == 0 || a.G == 1;
   p.f = ssm_params(a, dt_softplus != 0, cu_seqlens, num_seqs, init);
-  // blocks of the gradients' kernel: 256 / (threads per channel) channels each
-  const int ch = 256 / sm::threads_per_channel(static_cast<int>(a.N));
+  const int ch = sm::bwd_channels(static_cast<int>(a.N));
   p.f.blocks_per_group = static_cast<int>((a.C / a.G + ch - 1) / ch);
   const int64_t blocks = a.G * p.f.blocks_per_group;
   const size_t cn = static_cast<size_t>(a.C) * a.N;
@@ -284,7 +281,6 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.ddt_st = vddt.st;
   p.dz_st = vdz.st;
   p.dinit = static_cast<float*>(dinit);
-  p.wide = (even && aligned(vddt, pair) ? 1 : 0) | (even && aligned(vdu, pair) ? 2 : 0) | (even && aligned(vdz, pair) ? 4 : 0);
   sm::ReduceParams r;
   std::memset(&r, 0, sizeof(r));
   r.part_a = p.part_a;
