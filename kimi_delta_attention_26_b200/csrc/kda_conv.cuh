@@ -11,10 +11,13 @@
 // positions before the first token).
 //
 // Each input is read once and each output written once: bound by HBM. A warp
-// takes 32 x V channels (V = 16 bytes of them where strides and addresses
-// allow, else 1) of a run of tokens and carries the last inputs in registers.
+// takes 32 x V channels (V = 8 bytes of them, 16 for single tokens, where
+// strides and addresses allow, else 1) of a run of tokens, carries the last
+// inputs in registers and loads four tokens while it computes four.
 // All arithmetic is fp32; the outputs are rounded once.
 #pragma once
+
+#include <type_traits>
 
 #include "kda_io.cuh"
 
@@ -23,6 +26,7 @@ namespace conv {
 
 constexpr int NTHREADS = 128;
 constexpr int NWARPS = NTHREADS / 32;
+constexpr int RUN_BYTES = 8;  // of a row per access, prompts and gradients
 
 struct Params {
   const void* x;
@@ -39,13 +43,23 @@ struct Params {
   int silu;
 };
 
+// The weights of V channels, by tap. W = 4 comes as 16 bytes a channel where
+// the address allows.
 template <int V, int W>
 __device__ __forceinline__ void load_weights(float (&w)[W][V], float (&b)[V], const float* weight, const float* bias,
                                              int64_t c) {
+  const bool wide = W == 4 && reinterpret_cast<uintptr_t>(weight) % 16 == 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
+    if (wide) {
+      const float4 v = *reinterpret_cast<const float4*>(weight + (c + i) * W);
+      const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = weight[(c + i) * W + j];
+      for (int j = 0; j < W; ++j) w[j][i] = x[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = weight[(c + i) * W + j];
+    }
     b[i] = bias ? bias[c + i] : 0.f;
   }
 }
@@ -65,14 +79,31 @@ __device__ __forceinline__ void load_position(float (&x)[V], const T* x_base, in
   }
 }
 
+// acc += x * y, in pairs where there are any
+template <int V>
+__device__ __forceinline__ void fma_to(float (&acc)[V], const float (&x)[V], const float (&y)[V]) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 r = __ffma2_rn(make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]), make_float2(acc[i], acc[i + 1]));
+      acc[i] = r.x;
+      acc[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(x[i], y[i], acc[i]);
+  }
+}
+
+constexpr int KT = 4;  // tokens loaded together; the last inputs are a ring of KT rows, row t % KT
+
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(NTHREADS) conv_fwd_kernel(Params p) {
-  constexpr int KT = 8;  // tokens loaded together
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * V;
-  const T* x = static_cast<const T*>(p.x);
   const T* init = static_cast<const T*>(p.init);
   if (blockIdx.x >= p.run_blocks) {  // the sequences' states
+    const T* x = static_cast<const T*>(p.x);
     const int64_t s = (blockIdx.x - p.run_blocks) * NWARPS + warp;
     if (s >= p.N) return;
     if (blockIdx.y == 0 && lane == 0) check_packing(p.cu, static_cast<int>(s), p.T);
@@ -94,38 +125,63 @@ __global__ void __launch_bounds__(NTHREADS) conv_fwd_kernel(Params p) {
   if (c >= p.C) return;
   float w[W][V], b[V];
   load_weights<V, W>(w, b, p.weight, p.bias, c);
-  T* out = static_cast<T*>(p.out);
   for (int64_t pos = r0; s < p.N && pos < r1; ++s) {
     const int64_t start = bound(p.cu, s, p.T), lo = max(start, pos), hi = min(bound(p.cu, s + 1, p.T), r1);
     if (hi <= lo) continue;
     pos = hi;
-    float win[W + KT - 1][V];  // inputs t - W + 1 .. t + KT - 1
+    const T* x = static_cast<const T*>(p.x) + c + lo * p.x_st;  // the next token to load
+    T* out = static_cast<T*>(p.out) + c + lo * p.o_st;
+    float ring[KT][V];
 #pragma unroll
-    for (int i = 0; i < W - 1; ++i)
-      load_position<T, V, W>(win[i], x, p.x_st, init, p.C, c, s, start, lo - (W - 1) + i);
-    for (int64_t t = lo; t < hi; t += KT) {
-      Vec<T, V> raw[KT];
+    for (int i = 1; i < W; ++i)
+      load_position<T, V, W>(ring[KT - i], static_cast<const T*>(p.x), p.x_st, init, p.C, c, s, start, lo - i);
+    Vec<T, V> next[KT];
+    int left = static_cast<int>(hi - lo);  // tokens not yet loaded
+    auto fetch = [&] {
+      if (left >= KT) {
 #pragma unroll
-      for (int k = 0; k < KT; ++k)
-        if (t + k < hi) raw[k].load(x + (t + k) * p.x_st + c);
+        for (int k = 0; k < KT; ++k) next[k].load(x + k * p.x_st);
+      } else {
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        if (t + k >= hi) break;
-        float y[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          win[W - 1 + k][i] = raw[k].get(i);
-          float a = b[i];
-#pragma unroll
-          for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[k + j][i], a);
-          y[i] = p.silu ? silu(a) : a;
-        }
-        store_f32<T, V>(out + (t + k) * p.o_st + c, y);
+        for (int k = 0; k < KT; ++k)
+          if (k < left) next[k].load(x + k * p.x_st);
       }
+      x += KT * p.x_st;
+      left -= KT;
+    };
+    auto token = [&](int k) {
+      float a[V];
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i)
+      for (int i = 0; i < V; ++i) a[i] = b[i];
 #pragma unroll
-        for (int v = 0; v < V; ++v) win[i][v] = win[KT + i][v];
+      for (int j = 0; j < W; ++j) fma_to<V>(a, w[j], ring[(k + KT - (W - 1) + j) % KT]);
+      if (p.silu) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = silu(a[i]);
+      }
+      store_f32<T, V>(out + k * p.o_st, a);
+    };
+    fetch();
+    for (int todo = static_cast<int>(hi - lo); todo > 0; todo -= KT) {
+      Vec<T, V> now[KT];
+#pragma unroll
+      for (int k = 0; k < KT; ++k) now[k] = next[k];
+      if (left > 0) fetch();
+      if (todo >= KT) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+          now[k].get(ring[k]);
+          token(k);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+          if (k < todo) {
+            now[k].get(ring[k]);
+            token(k);
+          }
+      }
+      out += KT * p.o_st;
     }
   }
 }
@@ -142,37 +198,43 @@ struct DecodeParams {
   int silu;
 };
 
-// One thread: V channels of one request. It reads the W - 1 kept inputs and
-// the token before it writes any of them back, so out may be x itself.
+// One thread: V channels of every gridDim.y-th request, so that several requests
+// share one load of the weights. It reads the W - 1 kept inputs and the token
+// before it writes any of them back, so out may be x itself.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(NTHREADS) conv_decode_kernel(DecodeParams p) {
-  const int64_t b = blockIdx.x;
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * NTHREADS + threadIdx.x) * V;
-  int64_t slot = b;
-  if (p.idx) {
-    slot = p.idx[b];
-    if (slot < 0 || slot >= p.pool) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(&g_device_flags, KDA_DEVICE_BAD_STATE_INDEX);
-      return;
-    }
-  }
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * NTHREADS + threadIdx.x) * V;
   if (c >= p.C) return;
-  T* st = static_cast<T*>(p.state) + slot * (W - 1) * p.C + c;
-  Vec<T, V> raw[W];
+  float w[W][V], bias[V];
+  load_weights<V, W>(w, bias, p.weight, p.bias, c);
+  for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const int64_t slot = p.idx ? p.idx[b] : b;
+    if (slot < 0 || slot >= p.pool) {  // uniform over the block
+      if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_device_flags, KDA_DEVICE_BAD_STATE_INDEX);
+      continue;
+    }
+    T* st = static_cast<T*>(p.state) + slot * (W - 1) * p.C + c;
+    Vec<T, V> raw[W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) raw[j].load(st + j * p.C);
-  raw[W - 1].load(static_cast<const T*>(p.x) + b * p.x_st + c);
-  float w[W][V], y[V];
-  load_weights<V, W>(w, y, p.weight, p.bias, c);
+    for (int j = 0; j < W - 1; ++j) raw[j].load(st + j * p.C);
+    raw[W - 1].load(static_cast<const T*>(p.x) + b * p.x_st + c);
+    float y[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; ++i) y[i] = bias[i];
 #pragma unroll
-    for (int j = 0; j < W; ++j) y[i] = fmaf(w[j][i], raw[j].get(i), y[i]);
-    if (p.silu) y[i] = silu(y[i]);
+    for (int j = 0; j < W; ++j) {
+      float x[V];
+      raw[j].get(x);
+      fma_to<V>(y, w[j], x);
+    }
+    if (p.silu) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] = silu(y[i]);
+    }
+    store_f32<T, V>(static_cast<T*>(p.out) + b * p.o_st + c, y);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) raw[j + 1].store(st + j * p.C);
   }
-  store_f32<T, V>(static_cast<T*>(p.out) + b * p.o_st + c, y);
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) raw[j + 1].store(st + j * p.C);
 }
 
 // ---------------------------------------------------------------- backward
@@ -193,20 +255,11 @@ struct BwdParams {
   int silu;
 };
 
-// dp at a token whose W inputs are win[0 .. W - 1]
-template <int V, int W>
-__device__ __forceinline__ void pre_gradient(float (&dp)[V], const float (&dy)[V], const float (*win)[V],
-                                             const float (&w)[W][V], const float (&b)[V], int act) {
+// dp at a token with the activation's input a
+template <int V>
+__device__ __forceinline__ void pre_gradient(float (&dp)[V], const float (&dy)[V], const float (&a)[V], int act) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    dp[i] = dy[i];
-    if (act) {
-      float a = b[i];
-#pragma unroll
-      for (int j = 0; j < W; ++j) a = fmaf(w[j][i], win[j][i], a);
-      dp[i] *= dsilu(a);
-    }
-  }
+  for (int i = 0; i < V; ++i) dp[i] = act ? dy[i] * dsilu(a[i]) : dy[i];
 }
 
 // A warp walks its run of tokens forwards: at token t it has the inputs
@@ -215,7 +268,6 @@ __device__ __forceinline__ void pre_gradient(float (&dp)[V], const float (&dy)[V
 // the last dx; those tokens add nothing to its sums for dw and dbias.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(NTHREADS) conv_bwd_kernel(BwdParams p) {
-  constexpr int KT = 4;
   __shared__ float s_part[NWARPS][W + 1][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * V;
@@ -250,9 +302,13 @@ __global__ void __launch_bounds__(NTHREADS) conv_bwd_kernel(BwdParams p) {
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
       if (start + k >= end) break;
-      float dy[V], dp[V];
+      float dy[V], dp[V], a[V];
       load_f32<T, V>(dy, dout + (start + k) * p.d_st + c);
-      pre_gradient<V, W>(dp, dy, &win[k], w, b, p.silu);
+#pragma unroll
+      for (int v = 0; v < V; ++v) a[v] = b[v];
+#pragma unroll
+      for (int j = 0; j < W; ++j) fma_to<V>(a, w[j], win[k + j]);
+      pre_gradient<V>(dp, dy, a, p.silu);
       // token start + k sees position start - (W - 1) + i by tap j = i - k
 #pragma unroll
       for (int i = k; i < W - 1; ++i)
@@ -275,80 +331,108 @@ __global__ void __launch_bounds__(NTHREADS) conv_bwd_kernel(BwdParams p) {
     for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
   }
   if (c < p.C && r0 < r1) {
-    T* dx = static_cast<T*>(p.dx);
     load_weights<V, W>(w, b, p.weight, p.bias, c);
     const float zero[V] = {};
     int64_t pos = r0;
+    auto clear = [&](int64_t to) {  // tokens of no sequence
+      for (; pos < to; ++pos) store_f32<T, V>(static_cast<T*>(p.dx) + pos * p.g_st + c, zero);
+    };
     for (; s < p.N && pos < r1; ++s) {
       const int64_t start = bound(p.cu, s, p.T), end = bound(p.cu, s + 1, p.T);
       const int64_t lo = max(start, pos), hi = min(end, r1);
       if (hi <= lo) continue;
-      for (; pos < lo; ++pos) store_f32<T, V>(dx + pos * p.g_st + c, zero);  // tokens of no sequence
+      clear(lo);
       pos = hi;
-      float win[W + KT - 1][V], dp[W + KT - 1][V];  // inputs t - W + 1 ..; dp of the same tokens
+      // rings of the last inputs and of their dp; 0 before lo: no dx there is this warp's
+      float ring[KT][V], dp[KT][V];
 #pragma unroll
-      for (int i = 0; i < W - 1; ++i) {
-        load_position<T, V, W>(win[i], x, p.x_st, init, p.C, c, s, start, lo - (W - 1) + i);
+      for (int i = 1; i < W; ++i)
+        load_position<T, V, W>(ring[KT - i], x, p.x_st, init, p.C, c, s, start, lo - i);
 #pragma unroll
-        for (int v = 0; v < V; ++v) dp[i][v] = 0.f;
-      }
-      const int64_t stop = hi + W - 1;
-      for (int64_t t = lo; t < stop; t += KT) {
-        Vec<T, V> rx[KT], rd[KT];
+      for (int k = 0; k < KT; ++k)
 #pragma unroll
-        for (int k = 0; k < KT; ++k)
-          if (t + k < stop && t + k < end) {
-            rx[k].load(x + (t + k) * p.x_st + c);
-            rd[k].load(dout + (t + k) * p.d_st + c);
+        for (int v = 0; v < V; ++v) dp[k][v] = 0.f;
+      const int own = static_cast<int>(hi - lo);                              // tokens of the run
+      const int real = own + static_cast<int>(min(end - hi, static_cast<int64_t>(W - 1)));  // and those seen past it
+      const T* xp = x + c + lo * p.x_st;
+      const T* yp = dout + c + lo * p.d_st;
+      T* dx = static_cast<T*>(p.dx) + c + (lo - (W - 1)) * p.g_st;  // dx of the first token's oldest input
+      const int to_final = static_cast<int>(min(end - lo, static_cast<int64_t>(INT32_MAX)));  // token lo + to_final is the end
+      Vec<T, V> nx[KT], ny[KT];
+      int left = real;
+      auto fetch = [&] {
+        if (left >= KT) {
+#pragma unroll
+          for (int k = 0; k < KT; ++k) {
+            nx[k].load(xp + k * p.x_st);
+            ny[k].load(yp + k * p.d_st);
           }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KT; ++k)
+            if (k < left) {
+              nx[k].load(xp + k * p.x_st);
+              ny[k].load(yp + k * p.d_st);
+            }
+        }
+        xp += KT * p.x_st;
+        yp += KT * p.d_st;
+        left -= KT;
+      };
+      fetch();
+      for (int t = 0; t < own + W - 1; t += KT) {
+        Vec<T, V> cx[KT], cy[KT];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-          if (t + k >= stop) break;
-          float (&now)[V] = dp[W - 1 + k];
-          if (t + k < end) {
-            float dy[V];
+          cx[k] = nx[k];
+          cy[k] = ny[k];
+        }
+        if (left > 0) fetch();
+        // FULL: four tokens of the run whose dx are tokens of the run too, none of them in the final state
+        auto step = [&](int k, auto full) {
+          if (full.value || t + k < real) {
+            float dy[V], a[V];
+            cx[k].get(ring[k]);
+            cy[k].get(dy);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-              win[W - 1 + k][v] = rx[k].get(v);
-              dy[v] = rd[k].get(v);
-            }
-            pre_gradient<V, W>(now, dy, &win[k], w, b, p.silu);
-            if (t + k < hi) {
+            for (int v = 0; v < V; ++v) a[v] = b[v];
 #pragma unroll
-              for (int v = 0; v < V; ++v) {
-                db[v] += now[v];
+            for (int j = 0; j < W; ++j) fma_to<V>(a, w[j], ring[(k + KT - (W - 1) + j) % KT]);
+            pre_gradient<V>(dp[k], dy, a, p.silu);
+            if (full.value || t + k < own) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) dw[j][v] = fmaf(now[v], win[k + j][v], dw[j][v]);
-              }
+              for (int v = 0; v < V; ++v) db[v] += dp[k][v];
+#pragma unroll
+              for (int j = 0; j < W; ++j) fma_to<V>(dw[j], dp[k], ring[(k + KT - (W - 1) + j) % KT]);
             }
           } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) now[v] = 0.f;
+            for (int v = 0; v < V; ++v) dp[k][v] = 0.f;
           }
-          const int64_t at = t + k - (W - 1);
-          if (at >= lo) {
+          const int at = t + k - (W - 1);  // the token whose dx is complete, from lo
+          if (full.value || (at >= 0 && at < own)) {
             float g[V];
-            const int64_t row = at - (end - (W - 1));
 #pragma unroll
             for (int v = 0; v < V; ++v) g[v] = 0.f;
-            if (dfin && row >= 0) load_f32<T, V>(g, dfin + (static_cast<int64_t>(s) * (W - 1) + row) * p.C + c);
+            const int row = at - (to_final - (W - 1));
+            if (!full.value && dfin && row >= 0)
+              load_f32<T, V>(g, dfin + (static_cast<int64_t>(s) * (W - 1) + row) * p.C + c);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-              for (int j = 0; j < W; ++j) g[v] = fmaf(w[j][v], dp[W - 1 + k - j][v], g[v]);
-            store_f32<T, V>(dx + at * p.g_st + c, g);
+            for (int j = 0; j < W; ++j) fma_to<V>(g, w[j], dp[(k + KT - j) % KT]);
+            store_f32<T, V>(dx + k * p.g_st, g);
           }
+        };
+        if (t >= W - 1 && t + KT <= own && t + KT <= to_final - (W - 1)) {
+#pragma unroll
+          for (int k = 0; k < KT; ++k) step(k, std::true_type());
+        } else {
+#pragma unroll
+          for (int k = 0; k < KT; ++k) step(k, std::false_type());
         }
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            win[i][v] = win[KT + i][v];
-            dp[i][v] = dp[KT + i][v];
-          }
+        dx += KT * p.g_st;
       }
     }
-    for (; pos < r1; ++pos) store_f32<T, V>(dx + pos * p.g_st + c, zero);
+    clear(r1);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {

@@ -112,7 +112,7 @@ kda_status_t check_packing_args(const int32_t* cu, int32_t num_seqs, int64_t T) 
 bool aligned(const RowView& v, int64_t bytes) {
   return v.span.at % bytes == 0 && v.span.step % bytes == 0 && v.sg * v.eb % bytes == 0;
 }
-bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // f(the launches of the type)
 template <typename F>
@@ -185,8 +185,9 @@ kda_status_t kda_conv_fwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   if (any_overlap({a.out.span, s_fin}, {a.x.span, s_init, a.weight_span, a.bias_span})) return KDA_ERR_OVERLAP;
   int dev = 0;
   if ((st = prologue(&dev)) != KDA_OK) return st;
-  const int eb = io_bytes(a.dt), V = 16 / eb;
-  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && wide(init) && wide(fin);
+  constexpr int RB = cv::RUN_BYTES;
+  const int V = RB / io_bytes(a.dt);
+  const bool vec = a.C % V == 0 && aligned(a.x, RB) && aligned(a.out, RB) && aligned(init, RB) && aligned(fin, RB);
   const int64_t cb = (a.C + 32 * (vec ? V : 1) - 1) / (32 * (vec ? V : 1));
   cv::Params p;
   p.x = a.x.data;
@@ -200,7 +201,7 @@ kda_status_t kda_conv_fwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   p.C = a.C;
   p.x_st = a.x.st;
   p.o_st = a.out.st;
-  p.run = conv_run(a.T, cb, dev, 8, 64);
+  p.run = conv_run(a.T, cb, dev, 8, 128);
   p.run_blocks = (a.T + p.run * cv::NWARPS - 1) / (p.run * cv::NWARPS);
   p.N = num_seqs;
   p.silu = activation == KDA_ACT_SILU;
@@ -234,8 +235,8 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
   int dev = 0;
   if ((st = prologue(&dev)) != KDA_OK) return st;
   if (B == 0) return KDA_OK;
-  const int eb = io_bytes(a.dt), V = 16 / eb;
-  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && wide(sp);
+  const int V = 16 / io_bytes(a.dt);
+  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && aligned(sp, 16);
   cv::DecodeParams p;
   p.x = a.x.data;
   p.weight = static_cast<const float*>(a.weight);
@@ -249,8 +250,10 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
   p.o_st = a.out.st;
   p.pool = pool;
   p.silu = activation == KDA_ACT_SILU;
+  // enough blocks to fill the device; each takes every grid.y-th request
   const int per = cv::NTHREADS * (vec ? V : 1);
-  const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>((a.C + per - 1) / per));
+  const int64_t cb = (a.C + per - 1) / per, rows = std::max<int64_t>(1, int64_t(8) * g_num_sms[dev] / cb);
+  const dim3 grid(static_cast<unsigned>(cb), static_cast<unsigned>(std::min({B, rows, int64_t(65535)})));
   const cudaError_t e = by_type(a.dt, [&](auto m) { return m.conv_decode(p, a.W, vec, grid, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
@@ -282,9 +285,10 @@ kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   int dev = 0;
   if ((st = prologue(&dev)) != KDA_OK) return st;
   if ((st = prepare_pool(dev)) != KDA_OK) return st;
-  const int eb = io_bytes(a.dt), V = 16 / eb;
-  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && aligned(g, 16) && wide(init) && wide(dfin) &&
-                   wide(dinit);
+  constexpr int RB = cv::RUN_BYTES;
+  const int V = RB / io_bytes(a.dt);
+  const bool vec = a.C % V == 0 && aligned(a.x, RB) && aligned(a.out, RB) && aligned(g, RB) && aligned(init, RB) &&
+                   aligned(dfin, RB) && aligned(dinit, RB);
   const int64_t cb = (a.C + 32 * (vec ? V : 1) - 1) / (32 * (vec ? V : 1));
   cv::BwdParams p;
   p.x = a.x.data;

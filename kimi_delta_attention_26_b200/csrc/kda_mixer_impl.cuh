@@ -11,15 +11,15 @@ namespace {
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// f(vector width, taps)
-template <typename T, typename F>
+// f(vector width of BYTES or one element, taps)
+template <typename T, int BYTES, typename F>
 void by_conv(int W, bool vec, F f) {
   auto width = [&](auto v) {
     if (W == 2) f(v, Int<2>());
     else if (W == 3) f(v, Int<3>());
     else f(v, Int<4>());
   };
-  if (vec) width(Int<16 / sizeof(T)>());
+  if (vec) width(Int<BYTES / sizeof(T)>());
   else width(Int<1>());
 }
 
@@ -44,7 +44,7 @@ cudaError_t allow_shared(K* kernel, size_t bytes) {
 
 template <typename T>
 cudaError_t Mixer<T>::conv_fwd(const conv::Params& p, int W, bool vec, dim3 grid, cudaStream_t stream) {
-  by_conv<T>(W, vec, [&](auto v, auto w) {
+  by_conv<T, conv::RUN_BYTES>(W, vec, [&](auto v, auto w) {
     conv::conv_fwd_kernel<T, v.value, w.value><<<grid, conv::NTHREADS, 0, stream>>>(p);
   });
   return cudaGetLastError();
@@ -52,7 +52,7 @@ cudaError_t Mixer<T>::conv_fwd(const conv::Params& p, int W, bool vec, dim3 grid
 
 template <typename T>
 cudaError_t Mixer<T>::conv_decode(const conv::DecodeParams& p, int W, bool vec, dim3 grid, cudaStream_t stream) {
-  by_conv<T>(W, vec, [&](auto v, auto w) {
+  by_conv<T, 16>(W, vec, [&](auto v, auto w) {
     conv::conv_decode_kernel<T, v.value, w.value><<<grid, conv::NTHREADS, 0, stream>>>(p);
   });
   return cudaGetLastError();
@@ -60,7 +60,7 @@ cudaError_t Mixer<T>::conv_decode(const conv::DecodeParams& p, int W, bool vec, 
 
 template <typename T>
 cudaError_t Mixer<T>::conv_bwd(const conv::BwdParams& p, int W, bool vec, dim3 grid, cudaStream_t stream) {
-  by_conv<T>(W, vec, [&](auto v, auto w) {
+  by_conv<T, conv::RUN_BYTES>(W, vec, [&](auto v, auto w) {
     conv::conv_bwd_kernel<T, v.value, w.value><<<grid, conv::NTHREADS, 0, stream>>>(p);
   });
   return cudaGetLastError();
