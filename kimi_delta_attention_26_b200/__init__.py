@@ -344,22 +344,29 @@ def kda_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, 
 
 # ------------------------------------------------- short convolution and scan
 _ACTIVATION = {None: 0, "silu": 1}
-_DESC = struct.Struct("@Pii4q4q")
-_PAD = (0, 0, 0, 0)
+_desc = struct.Struct("@Pii4q4q").pack
 
 
 def _pack(t: Optional[torch.Tensor], name: str, index: int):
     """``kda_tensor_t`` of a tensor on CUDA device `index`, as bytes (None -> NULL)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != index:
+    try:
+        on, n, code = t.get_device(), t.dim(), _DTYPE.get(t.dtype, 0)
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if on != index:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-    n = t.dim()
+    if n == 2:
+        (a, b), (p, q) = t.shape, t.stride()
+        return _desc(t.data_ptr(), 2, code, a, b, 0, 0, p, q, 0, 0)
+    if n == 3:
+        (a, b, c), (p, q, r) = t.shape, t.stride()
+        return _desc(t.data_ptr(), 3, code, a, b, c, 0, p, q, r, 0)
     if n > 4:
         raise ValueError(f"{name} has more than 4 dimensions")
-    return _DESC.pack(t.data_ptr(), n, _DTYPE.get(t.dtype, 0), *t.shape, *_PAD[n:], *t.stride(), *_PAD[n:])
+    pad = (0,) * (4 - n)
+    return _desc(t.data_ptr(), n, code, *t.shape, *pad, *t.stride(), *pad)
 
 
 def _device_of(t: torch.Tensor, name: str, dims: int, fn: str) -> int:
@@ -421,7 +428,12 @@ _HERE = _Here()
 def _on(index: int, stream: Optional[torch.cuda.Stream], tensors):
     if stream is not None:
         return _On(index, stream, tensors)
-    return _HERE if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return _HERE if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+
+
+def _rows_like(t: torch.Tensor) -> torch.Tensor:
+    """New contiguous rows of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _raise(code: int, checks) -> None:
@@ -461,7 +473,7 @@ def kda_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     (T, C), W = x.shape, weight.shape[1]
     with _on(dev, stream, (x, weight, bias, cu_seqlens, initial_state, out, final_state)):
         if out is None:
-            out = torch.empty((T, C), dtype=x.dtype, device=x.device)
+            out = _rows_like(x)
         if final_state is None and output_final_state:
             final_state = torch.empty((N, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
         rc = _lib.kda_conv_fwd(_pack(x, "x", dev), _pack(weight, "weight", dev), _pack(bias, "bias", dev), act, cu, N,
@@ -490,7 +502,7 @@ def kda_conv_decode(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
     idx = _int32_ptr(state_indices, "state_indices", dev, B)
     with _on(dev, stream, (x, weight, bias, state, state_indices, out)):
         if out is None:
-            out = torch.empty((B, C), dtype=x.dtype, device=x.device)
+            out = _rows_like(x)
         rc = _lib.kda_conv_decode(_pack(x, "x", dev), _pack(weight, "weight", dev), _pack(bias, "bias", dev), act,
                                   _pack(state, "state", dev), idx, _pack(out, "out", dev),
                                   torch._C._cuda_getCurrentRawStream(dev))
@@ -517,7 +529,7 @@ def kda_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bias
         raise ValueError("weight must be [C, W]")
     (T, C), W = x.shape, weight.shape[1]
     with _on(dev, stream, (x, weight, bias, cu_seqlens, initial_state, dout, dfinal_state)):
-        dx = torch.empty((T, C), dtype=x.dtype, device=x.device)
+        dx = _rows_like(x)
         dw = torch.empty((C, W), dtype=torch.float32, device=x.device)
         db = None if bias is None else torch.empty((C,), dtype=torch.float32, device=x.device)
         di = torch.empty((N, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
@@ -564,7 +576,7 @@ def kda_ssm_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Ten
     T, c = u.shape
     with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, out, final_state)):
         if out is None:
-            out = torch.empty((T, c), dtype=u.dtype, device=u.device)
+            out = _rows_like(u)
         if final_state is None and output_final_state:
             final_state = torch.empty((N, c, A.shape[-1]), dtype=torch.float32, device=u.device)
         rc = _lib.kda_ssm_fwd(_pack(u, "u", dev), _pack(dt, "dt", dev), _pack(A, "A", dev), _pack(B, "B", dev),
@@ -596,7 +608,7 @@ def kda_ssm_decode(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     idx = _int32_ptr(state_indices, "state_indices", dev, R)
     with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, state, state_indices, out)):
         if out is None:
-            out = torch.empty((R, c), dtype=u.dtype, device=u.device)
+            out = _rows_like(u)
         rc = _lib.kda_ssm_decode(_pack(u, "u", dev), _pack(dt, "dt", dev), _pack(A, "A", dev), _pack(B, "B", dev),
                                  _pack(C, "C", dev), _pack(D, "D", dev), _pack(z, "z", dev),
                                  _pack(dt_bias, "dt_bias", dev), bool(dt_softplus), _pack(state, "state", dev), idx,

@@ -98,7 +98,7 @@ cudaError_t Mixer<T>::scan(ssm::Params p, bool out, int ranges, int sms, cudaStr
 template <typename T>
 cudaError_t Mixer<T>::scan_decode(const ssm::DecodeParams& p, int64_t requests, cudaStream_t stream) {
   by_states(p.N, [&](auto l, auto) {
-    constexpr int CH = ssm::NTHREADS / l.value;
+    constexpr int CH = ssm::NTHREADS / l.value * 4;
     ssm::ssm_decode_kernel<T, l.value>
         <<<dim3(static_cast<unsigned>(requests), (p.C + CH - 1) / CH), ssm::NTHREADS, 0, stream>>>(p);
   });

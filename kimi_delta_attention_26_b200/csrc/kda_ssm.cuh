@@ -478,48 +478,104 @@ struct DecodeParams {
   int64_t u_st, dt_st, z_st, o_st, b_st, b_sg, c_st, c_sg;
   int C, N, G;
   int softplus;
+  int wide;                 // bits 0, 1, 2: rows of B, C, state and A can be moved four states at a time
 };
 
-// One block: 128 / L channels of one request.
+// One block: 512 / L channels of one request, four channels per group of L
+// threads; a thread holds four states of each, all loaded before any
+// arithmetic. The state is read and written once (8 bytes a state against about
+// 8 bytes of tokens a channel), so HBM bounds it. Thread j < 4 of a group
+// computes the step of the group's channel j for the others, and its output.
 template <typename T, int L>
 __global__ void __launch_bounds__(NTHREADS) ssm_decode_kernel(DecodeParams p) {
-  constexpr int CH = NTHREADS / L;
+  constexpr unsigned ALL = 0xffffffffu;
   const int64_t r = blockIdx.x;
-  const int q = threadIdx.x % L, ch = blockIdx.y * CH + threadIdx.x / L;
+  const int q = threadIdx.x % L, c0 = blockIdx.y * (NTHREADS / L * 4) + threadIdx.x / L * 4;
   int64_t slot = r;
   if (p.idx) {
     slot = p.idx[r];
-    if (slot < 0 || slot >= p.pool) {
+    if (slot < 0 || slot >= p.pool) {  // uniform over the block
       if (threadIdx.x == 0 && blockIdx.y == 0) atomicOr(&g_device_flags, KDA_DEVICE_BAD_STATE_INDEX);
       return;
     }
   }
-  const bool live = ch < p.C;
-  float y = 0.f, uu = 0.f;
-  if (live) {
-    const int group = ch / (p.C / p.G);
-    uu = to_f32(static_cast<const T*>(p.u)[r * p.u_st + ch]);
-    const float d = step_of<sizeof(T) == 4>(to_f32(static_cast<const T*>(p.dt)[r * p.dt_st + ch]) + (p.dt_bias ? p.dt_bias[ch] : 0.f),
-                            p.softplus);
-    const T* bb = static_cast<const T*>(p.b) + r * p.b_st + group * p.b_sg;
-    const T* cc = static_cast<const T*>(p.c) + r * p.c_st + group * p.c_sg;
-    float* st = p.state + (slot * p.C + ch) * p.N;
+  const int mine = c0 + (q & 3);
+  const bool owner = q < 4 && mine < p.C;
+  const bool wide = p.wide & 4;
+  const int n0 = q * S, nv = max(0, min(S, p.N - n0));
+  float h[4][S], a[4][S];
+  float* st = p.state + (slot * p.C + c0) * p.N + n0;
+  const float* A = p.A + static_cast<int64_t>(c0) * p.N + n0;
+  if (wide && nv == S && c0 + 4 <= p.C) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_f32<float, S>(h[j], st + static_cast<int64_t>(j) * p.N);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_f32<float, S>(a[j], A + static_cast<int64_t>(j) * p.N);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        const bool on = c0 + j < p.C && i < nv;
+        h[j][i] = on ? st[static_cast<int64_t>(j) * p.N + i] : 0.f;
+        a[j][i] = on ? A[static_cast<int64_t>(j) * p.N + i] : 0.f;
+      }
+  }
+  float uu = 0.f, raw = 0.f, gate = 1.f, skip = 0.f;
+  if (owner) {
+    uu = to_f32(static_cast<const T*>(p.u)[r * p.u_st + mine]);
+    raw = to_f32(static_cast<const T*>(p.dt)[r * p.dt_st + mine]) + (p.dt_bias ? p.dt_bias[mine] : 0.f);
+    if (p.z) gate = to_f32(static_cast<const T*>(p.z)[r * p.z_st + mine]);
+    if (p.D) skip = p.D[mine];
+  }
+  // a group's four channels may belong to different groups of B and C
+  const int cg = p.C / p.G;
+  float b[S], c[S];
+  int group = -1;
+  auto load_bc = [&](int g) {
+    Vec<T, S> vb[1], vc[1];
+    const bool all = nv == S;
+    load_rows(vb, static_cast<const T*>(p.b) + r * p.b_st + g * p.b_sg + n0, 0, nv, all && (p.wide & 1), [](int) { return 0; });
+    load_rows(vc, static_cast<const T*>(p.c) + r * p.c_st + g * p.c_sg + n0, 0, nv, all && (p.wide & 2), [](int) { return 0; });
+    vb[0].get(b);
+    vc[0].get(c);
+    group = g;
+  };
+  load_bc(min(c0, p.C - 1) / cg);
+  const float d = step_of<sizeof(T) == 4>(raw, p.softplus), du = d * uu;
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float dj = __shfl_sync(ALL, d, j, L), uj = __shfl_sync(ALL, du, j, L);
+    if (j && c0 + j < p.C && (c0 + j) / cg != group) load_bc((c0 + j) / cg);
+    y[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const int n = q * S + i;
-      if (n >= p.N) continue;
-      const float h = fmaf(exp2_approx(d * (p.A[static_cast<int64_t>(ch) * p.N + n] * kLog2e)), st[n],
-                           d * uu * to_f32(bb[n]));
-      st[n] = h;
-      y = fmaf(to_f32(cc[n]), h, y);
+      h[j][i] = fmaf(exp2_approx(dj * (a[j][i] * kLog2e)), h[j][i], uj * b[i]);
+      y[j] = fmaf(c[i], h[j][i], y[j]);
     }
   }
+  if (wide && nv == S && c0 + 4 <= p.C) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-  if (live && q == 0) {
-    if (p.D) y = fmaf(p.D[ch], uu, y);
-    if (p.z) y *= silu(to_f32(static_cast<const T*>(p.z)[r * p.z_st + ch]));
-    static_cast<T*>(p.out)[r * p.o_st + ch] = from_f32<T>(y);
+    for (int j = 0; j < 4; ++j) store_f32<float, S>(st + static_cast<int64_t>(j) * p.N, h[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+        if (c0 + j < p.C && i < nv) st[static_cast<int64_t>(j) * p.N + i] = h[j][i];
+  }
+  // over the group's threads: thread q ends with channel q % 4
+  const bool up2 = q & 2, up1 = q & 1;
+  const float y0 = (up2 ? y[2] : y[0]) + __shfl_xor_sync(ALL, up2 ? y[0] : y[2], 2);
+  const float y1 = (up2 ? y[3] : y[1]) + __shfl_xor_sync(ALL, up2 ? y[1] : y[3], 2);
+  float v = (up1 ? y1 : y0) + __shfl_xor_sync(ALL, up1 ? y0 : y1, 1);
+#pragma unroll
+  for (int o = 4; o < L; o <<= 1) v += __shfl_xor_sync(ALL, v, o);
+  if (owner) {
+    v = fmaf(skip, uu, v);
+    if (p.z) v *= silu(gate);
+    static_cast<T*>(p.out)[r * p.o_st + mine] = from_f32<T>(v);
   }
 }
 

@@ -211,6 +211,9 @@ kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const
   p.N = static_cast<int>(a.N);
   p.G = static_cast<int>(a.G);
   p.softplus = dt_softplus != 0;
+  const int quad = 4 * io_bytes(a.dt);
+  p.wide = (a.N % 4 == 0 && aligned(a.b, quad) ? 1 : 0) | (a.N % 4 == 0 && aligned(a.c, quad) ? 2 : 0) |
+           (a.N % 4 == 0 && aligned(sp, 16) && aligned(a.A, 16) ? 4 : 0);
   const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan_decode(p, B_, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }

@@ -177,6 +177,31 @@ def test_conv_strided_and_unaligned_views(kda):
         assert torch.equal(gr["dx"], rg["dx"]) and torch.equal(gr["dinitial_state"], rg["dinitial_state"])
 
 
+def test_conv_states_and_parameters_at_any_address(kda):
+    lens, C = [31, 9], 64
+    d = make(lens, C, 4, torch.float16, seed=15)
+    cu = cu_of(lens)
+
+    def off(t):
+        v = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        v.copy_(t)
+        return v
+
+    e = {k: off(v) for k, v in d.items()}
+    a = kda.kda_conv_fwd(d["x"], d["weight"], d["bias"], cu_seqlens=cu, initial_state=d["init"])
+    b = kda.kda_conv_fwd(e["x"], e["weight"], e["bias"], cu_seqlens=cu, initial_state=e["init"])
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    ga = kda.kda_conv_bwd(d["x"], d["weight"], d["dout"], d["bias"], "silu", cu, d["init"], d["dfin"])
+    gb = kda.kda_conv_bwd(e["x"], e["weight"], e["dout"], e["bias"], "silu", cu, e["init"], e["dfin"])
+    assert torch.equal(ga["dx"], gb["dx"]) and torch.equal(ga["dinitial_state"], gb["dinitial_state"])
+    for k in ("dweight", "dbias"):  # other runs of tokens, another order of the sums: 40 of at most 40 roundings
+        assert torch.allclose(ga[k], gb[k], rtol=1e-4, atol=1e-4)
+    s1, s2 = d["init"].clone(), off(d["init"])
+    o1 = kda.kda_conv_decode(d["x"][:2], d["weight"], s1, d["bias"])
+    o2 = kda.kda_conv_decode(off(d["x"][:2]), e["weight"], s2, e["bias"])
+    assert torch.equal(o1, o2) and torch.equal(s1, s2)
+
+
 def test_conv_bad_boundaries_are_recorded(kda):
     """Boundaries that are no packing: every access is clamped, the status word tells."""
     d = make([60], 72, 4, torch.bfloat16, seed=6)

@@ -309,6 +309,35 @@ def test_scan_strided_views(kda):
             assert torch.equal(gr[k], rg[k]), k
 
 
+def test_scan_states_and_parameters_at_any_address(kda):
+    """States, A and the other parameters at 4-byte addresses: the bits of aligned ones."""
+    lens, c, n = [30, 11], 40, 16
+    d = make(lens, c, n, 1, torch.bfloat16, seed=51)
+    cu = cu_of(lens)
+
+    def off(t, fill=None):
+        buf = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        v = buf[1:].view(t.shape)
+        v.copy_(t)
+        return v
+
+    e = dict(d)
+    for k in ("A", "D", "bias", "init", "dfin"):
+        e[k] = off(d[k])
+    a = fwd(kda, d, cu, initial_state=d["init"])
+    b = fwd(kda, e, cu, initial_state=e["init"], final_state=off(d["init"]))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    ga = bwd(kda, d, cu, initial_state=d["init"], dfinal_state=d["dfin"])
+    gb = bwd(kda, e, cu, initial_state=e["init"], dfinal_state=e["dfin"])
+    assert all(torch.equal(ga[k], gb[k]) for k in ga)
+    r = slice(0, 2)
+    args = lambda x: (x["u"][r], x["dt"][r], x["A"], x["B"][r], x["C"][r])  # noqa: E731
+    s1, s2 = d["init"].clone(), off(d["init"])
+    o1 = kda.kda_ssm_decode(*args(d), s1, d["D"], d["z"][r], d["bias"])
+    o2 = kda.kda_ssm_decode(*args(e), s2, e["D"], e["z"][r], e["bias"])
+    assert torch.equal(o1, o2) and torch.equal(s1, s2)
+
+
 def test_scan_bad_boundaries_are_recorded(kda):
     d = make([60], 40, 16, 1, torch.bfloat16, state=False, seed=6)
     for bad in ([0, 50, 20, 60], [0, 30, 99, 10 ** 9], [-5, 10, 40, 60], [4, 10, 40, 60]):
