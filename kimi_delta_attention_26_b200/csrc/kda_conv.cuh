@@ -207,17 +207,30 @@ __global__ void __launch_bounds__(NTHREADS) conv_decode_kernel(DecodeParams p) {
   if (c >= p.C) return;
   float w[W][V], bias[V];
   load_weights<V, W>(w, bias, p.weight, p.bias, c);
-  for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
-    const int64_t slot = p.idx ? p.idx[b] : b;
-    if (slot < 0 || slot >= p.pool) {  // uniform over the block
+  // the next request's rows are loaded before this one's arithmetic
+  Vec<T, V> next[W];
+  int64_t next_slot = -1;
+  auto fetch = [&](int64_t b) {
+    next_slot = p.idx ? p.idx[b] : b;
+    if (next_slot < 0 || next_slot >= p.pool) {  // uniform over the block
       if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_device_flags, KDA_DEVICE_BAD_STATE_INDEX);
-      continue;
+      next_slot = -1;
+      return;
     }
-    T* st = static_cast<T*>(p.state) + slot * (W - 1) * p.C + c;
+    const T* st = static_cast<const T*>(p.state) + next_slot * (W - 1) * p.C + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) next[j].load(st + j * p.C);
+    next[W - 1].load(static_cast<const T*>(p.x) + b * p.x_st + c);
+  };
+  fetch(blockIdx.y);
+  for (int64_t b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const int64_t slot = next_slot;
     Vec<T, V> raw[W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) raw[j].load(st + j * p.C);
-    raw[W - 1].load(static_cast<const T*>(p.x) + b * p.x_st + c);
+    for (int j = 0; j < W; ++j) raw[j] = next[j];
+    if (b + gridDim.y < p.B) fetch(b + gridDim.y);
+    if (slot < 0) continue;
+    T* st = static_cast<T*>(p.state) + slot * (W - 1) * p.C + c;
     float y[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) y[i] = bias[i];

@@ -235,8 +235,9 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
   int dev = 0;
   if ((st = prologue(&dev)) != KDA_OK) return st;
   if (B == 0) return KDA_OK;
-  const int V = 16 / io_bytes(a.dt);
-  const bool vec = a.C % V == 0 && aligned(a.x, 16) && aligned(a.out, 16) && aligned(sp, 16);
+  constexpr int RB = cv::RUN_BYTES;
+  const int V = RB / io_bytes(a.dt);
+  const bool vec = a.C % V == 0 && aligned(a.x, RB) && aligned(a.out, RB) && aligned(sp, RB);
   cv::DecodeParams p;
   p.x = a.x.data;
   p.weight = static_cast<const float*>(a.weight);

@@ -52,7 +52,7 @@ cudaError_t Mixer<T>::conv_fwd(const conv::Params& p, int W, bool vec, dim3 grid
 
 template <typename T>
 cudaError_t Mixer<T>::conv_decode(const conv::DecodeParams& p, int W, bool vec, dim3 grid, cudaStream_t stream) {
-  by_conv<T, 16>(W, vec, [&](auto v, auto w) {
+  by_conv<T, conv::RUN_BYTES>(W, vec, [&](auto v, auto w) {
     conv::conv_decode_kernel<T, v.value, w.value><<<grid, conv::NTHREADS, 0, stream>>>(p);
   });
   return cudaGetLastError();
