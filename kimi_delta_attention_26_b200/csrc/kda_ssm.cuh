@@ -677,17 +677,47 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
   const float skip = p.D && c0 + xc < c_end ? p.D[c0 + xc] : 0.f;
   float sum_d = 0.f, sum_bias = 0.f;
   const int64_t tiles = (end - start + TB - 1) / TB;
-  for (int64_t k = tiles - 1; k >= 0; --k) {
-    const int64_t t0 = start + k * TB;
+  // A tile's rows as they came and the state kept before its last half: loaded
+  // while the tile after it is finished.
+  constexpr int NB = (TB * L + NT - 1) / NT;
+  Vec<T, 2> vu[TG], vd[TG], vz[TG], vo[TG];
+  Vec<T, 4> vb[NB], vc[NB];
+  float kept[4] = {0.f, 0.f, 0.f, 0.f};
+  const int64_t kept0 = (first_kept(start, seq) * p.C + ch) * p.N + q * 4;
+  auto load_kept = [&](int64_t tile, int half) {
+    const int64_t at = kept0 + (tile * (TB / KT) + half) * cn;
+    if (p.N % 4 == 0) {
+      if (live && q * 4 < p.N) load_f32<float, 4>(kept, p.ck + at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (live && q * 4 + i < p.N) kept[i] = p.ck[at + i];
+    }
+  };
+  const int n0 = tid % L * 4, nv = max(0, min(4, p.N - n0));
+  auto load_tile = [&](int64_t tile) {
+    const int64_t t0 = start + tile * TB;
     const int nt = static_cast<int>(min(static_cast<int64_t>(TB), end - t0));
-    // ------------------------------------------------ the tile's operands
     if (m0 < TB) {
-      Vec<T, 2> vu[TG], vd[TG], vz[TG], vo[TG];
       auto tok = [&](int j) { return t0 + min(m0 + j, nt - 1); };
       load_rows(vd, static_cast<const T*>(p.dt) + mc, p.dt_st, valid, (p.wide & 2) && valid == 2, tok);
       load_rows(vu, static_cast<const T*>(p.u) + mc, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
       load_rows(vo, static_cast<const T*>(bp.dout) + mc, bp.dout_st, valid, (p.wide & 32) && valid == 2, tok);
       if (p.z) load_rows(vz, static_cast<const T*>(p.z) + mc, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
+    }
+    if (tid < TB * L) {
+      auto tok = [&](int j) { return t0 + min((tid + j * NT) / L, nt - 1); };
+      load_rows(vb, static_cast<const T*>(p.b) + group * p.b_sg + n0, p.b_st, nv, (p.wide & 8) && nv == 4, tok);
+      load_rows(vc, static_cast<const T*>(p.c) + group * p.c_sg + n0, p.c_st, nv, (p.wide & 16) && nv == 4, tok);
+    }
+    load_kept(tile, nt > KT ? 1 : 0);
+  };
+  if (tiles > 0) load_tile(tiles - 1);
+  for (int64_t k = tiles - 1; k >= 0; --k) {
+    const int64_t t0 = start + k * TB;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(TB), end - t0));
+    // ------------------------------------------------ the tile's operands
+    if (m0 < TB) {
 #pragma unroll
       for (int j = 0; j < TG; ++j) {
         const int t = m0 + j;
@@ -715,22 +745,22 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
         if (p.z) sm.zf[t][mp] = make_float2(zf[0], zf[1]);
       }
     }
+    if (tid < TB * L) {
 #pragma unroll
-    for (int i = tid; i < TB * L; i += NT) {
-      const int t = i / L, n0 = i % L * 4, nv = t < nt ? max(0, min(4, p.N - n0)) : 0;
-      const int64_t tt = t0 + min(t, nt - 1);
-      Vec<T, 4> vb[1], vc[1];
-      load_rows(vb, static_cast<const T*>(p.b) + group * p.b_sg + n0, p.b_st, nv, (p.wide & 8) && nv == 4,
-                [&](int) { return tt; });
-      load_rows(vc, static_cast<const T*>(p.c) + group * p.c_sg + n0, p.c_st, nv, (p.wide & 16) && nv == 4,
-                [&](int) { return tt; });
-      float fb[4], fc[4];
-      vb[0].get(fb);
-      vc[0].get(fc);
+      for (int j = 0; j < NB; ++j) {
+        const int t = (tid + j * NT) / L;
+        float fb[4], fc[4];
+        vb[j].get(fb);
+        vc[j].get(fc);
+        if (t >= nt) {
 #pragma unroll
-      for (int o = 0; o < FB; ++o) {
-        *reinterpret_cast<float4*>(&sm.b[t][o][n0]) = make_float4(fb[0 ^ o], fb[1 ^ o], fb[2 ^ o], fb[3 ^ o]);
-        *reinterpret_cast<float4*>(&sm.c[t][o][n0]) = make_float4(fc[0 ^ o], fc[1 ^ o], fc[2 ^ o], fc[3 ^ o]);
+          for (int i = 0; i < 4; ++i) fb[i] = fc[i] = 0.f;
+        }
+#pragma unroll
+        for (int o = 0; o < FB; ++o) {
+          *reinterpret_cast<float4*>(&sm.b[t][o][n0]) = make_float4(fb[0 ^ o], fb[1 ^ o], fb[2 ^ o], fb[3 ^ o]);
+          *reinterpret_cast<float4*>(&sm.c[t][o][n0]) = make_float4(fc[0 ^ o], fc[1 ^ o], fc[2 ^ o], fc[3 ^ o]);
+        }
       }
     }
     __syncthreads();
@@ -740,22 +770,14 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
     for (int half = 1; half >= 0; --half) {
       if (half * KT >= nt) continue;
       float2 h0[2], e[KT][2], h[KT][2];
-      {
-        const int64_t at = ((first_kept(start, seq) + k * (TB / KT) + half) * p.C + ch) * p.N + q * 4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (p.N % 4 == 0) {
-          if (live && q * 4 < p.N) load_f32<float, 4>(v, p.ck + at);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (live && q * 4 + i < p.N) v[i] = p.ck[at + i];
-        }
-        // into the lane's order
+      {  // the kept state, into the lane's order
+        const float* v = kept;
         const bool f0 = f & 1, f1 = f & 2;
         const float w0 = f0 ? v[1] : v[0], w1 = f0 ? v[0] : v[1], w2 = f0 ? v[3] : v[2], w3 = f0 ? v[2] : v[3];
         h0[0] = f1 ? make_float2(w2, w3) : make_float2(w0, w1);
         h0[1] = f1 ? make_float2(w0, w1) : make_float2(w2, w3);
       }
+      if (half == 1) load_kept(k, 0);
       const float2* const dp = &sm.d[half * KT][chl];
       const float* const yp = &sm.dy[half * KT][chl];
       const float* const bq = &sm.b[half * KT][f][q * 4];
@@ -852,6 +874,7 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
     }
     __syncthreads();
     // ------------------------------------------------------- the gradients
+    if (k > 0) load_tile(k - 1);
     for (int i = tid; i < nt * NP; i += NT) {
       const int t = i / NP, n = i % NP;
       if (n >= p.N) continue;
