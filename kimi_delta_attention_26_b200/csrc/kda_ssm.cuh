@@ -8,6 +8,8 @@
 //   y_t = sum_n C_t[g, n] h_t[n] + D u_t,   out_t = y_t or y_t z_t sigmoid(z_t)
 #pragma once
 
+#include <type_traits>
+
 #include "kda_io.cuh"
 
 namespace kda {
@@ -324,7 +326,26 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
     Vec<T, S> rb[NB], rc[NB];
     // rows past the piece's end: its last one again, set to 0 below
     const int n0 = tid % L * S, nv = max(0, min(S, p.N - n0));
+    const bool all = (p.wide & 1) && (p.wide & 2) && (p.wide & 8) && (p.wide & 16) && valid == 2 && nv == S &&
+                     TT % TK == 0 && TT * L % ROLE == 0;
     auto load = [&](int64_t t0, int nt) {
+      if (all && nt == TT) {  // nothing to check
+        const T* pu = u + (t0 + tk) * p.u_st;
+        const T* pd = dt + (t0 + tk) * p.dt_st;
+        const T* pb = bb + n0 + (t0 + tid / L) * p.b_st;
+        const T* pc = cc + n0 + (t0 + tid / L) * p.c_st;
+#pragma unroll
+        for (int k = 0; k < NU; ++k, pu += TK * p.u_st, pd += TK * p.dt_st) {
+          ru[k].load(pu);
+          rd[k].load(pd);
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k, pb += ROLE / L * p.b_st, pc += ROLE / L * p.c_st) {
+          rb[k].load(pb);
+          if (OUT) rc[k].load(pc);
+        }
+        return;
+      }
       auto tok = [&](int k) { return t0 + min(tk + k * TK, nt - 1); };
       auto bct = [&](int k) { return t0 + min((tid + k * ROLE) / L, nt - 1); };
       load_rows(ru, u, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
@@ -398,6 +419,18 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
     for (int i = 0; i < 2; ++i) skip[i] = p.D && i < valid ? p.D[c0 + k0 + i] : 0.f;
     Vec<T, 2> ru[4 * NG], rz[4 * NG];
     auto load = [&](int64_t t0, int nt) {
+      if ((p.wide & 1) && (p.wide & 4) && valid == 2 && nt == TT && p.D && p.z && TT / 4 % GK == 0) {  // nothing to check
+        const T* pu = u + (t0 + tk * 4) * p.u_st;
+        const T* pz = z + (t0 + tk * 4) * p.z_st;
+#pragma unroll
+        for (int g = 0; g < NG; ++g, pu += 4 * GK * p.u_st, pz += 4 * GK * p.z_st)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ru[g * 4 + j].load(pu + j * p.u_st);
+            rz[g * 4 + j].load(pz + j * p.z_st);
+          }
+        return;
+      }
       auto tok = [&](int k) { return t0 + min((tk + k / 4 * GK) * 4 + k % 4, nt - 1); };
       if (p.D) load_rows(ru, u, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
       if (p.z) load_rows(rz, z, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
@@ -417,41 +450,46 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
           }
         if (t0 + TT < hi) load(t0 + TT, static_cast<int>(min(static_cast<int64_t>(TT), hi - t0 - TT)));
         mbar_wait(&sm.y_full[yr.slot], yr.phase);
+        // whole: a full tile of full pairs, nothing to check
+        auto write = [&](auto whole) {
+          T* row = out + (t0 + tk * 4) * p.o_st;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          const int tg = tk + g * GK;
-          if (tg * 4 >= nt) break;
-          float4 even = make_float4(0.f, 0.f, 0.f, 0.f), odd = even;
-          const unsigned char* yp = &sm.y[yr.slot][tg][0][k0 / 2 * 16];
+          for (int g = 0; g < NG; ++g, row += 4 * GK * p.o_st) {
+            const int tg = tk + g * GK;
+            if (!(whole.value && TT / 4 % GK == 0) && tg * 4 >= nt) break;
+            float4 even = make_float4(0.f, 0.f, 0.f, 0.f), odd = even;
+            const unsigned char* yp = &sm.y[yr.slot][tg][0][k0 / 2 * 16];
 #pragma unroll
-          for (int l = 0; l < L; ++l) {
-            const float4 a = *reinterpret_cast<const float4*>(yp + l * Sh::QS);
-            const float4 b = *reinterpret_cast<const float4*>(yp + l * Sh::QS + Sh::ODD);
-            even.x += a.x;
-            even.y += a.y;
-            even.z += a.z;
-            even.w += a.w;
-            odd.x += b.x;
-            odd.y += b.y;
-            odd.z += b.z;
-            odd.w += b.w;
-          }
-          const float ev[4] = {even.x, even.y, even.z, even.w}, od[4] = {odd.x, odd.y, odd.z, odd.w};
+            for (int l = 0; l < L; ++l) {
+              const float4 a = *reinterpret_cast<const float4*>(yp + l * Sh::QS);
+              const float4 b = *reinterpret_cast<const float4*>(yp + l * Sh::QS + Sh::ODD);
+              even.x += a.x;
+              even.y += a.y;
+              even.z += a.z;
+              even.w += a.w;
+              odd.x += b.x;
+              odd.y += b.y;
+              odd.z += b.z;
+              odd.w += b.w;
+            }
+            const float ev[4] = {even.x, even.y, even.z, even.w}, od[4] = {odd.x, odd.y, odd.z, odd.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int t = tg * 4 + j, k = g * 4 + j;
-            if (t >= nt) break;
-            const float y[2] = {(ev[j] + du[k][0]) * gate[k][0], (od[j] + du[k][1]) * gate[k][1]};
-            T* to = out + (t0 + t) * p.o_st;
-            if ((p.wide & 32) && valid == 2) {
-              store_f32<T, 2>(to, y);
-            } else {
+            for (int j = 0; j < 4; ++j) {
+              const int k = g * 4 + j;
+              const float y[2] = {(ev[j] + du[k][0]) * gate[k][0], (od[j] + du[k][1]) * gate[k][1]};
+              T* to = row + j * p.o_st;
+              if (whole.value) {
+                store_f32<T, 2>(to, y);
+              } else if (tg * 4 + j < nt) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (i < valid) to[i] = from_f32<T>(y[i]);
+                for (int i = 0; i < 2; ++i)
+                  if (i < valid) to[i] = from_f32<T>(y[i]);
+              }
             }
           }
-        }
+        };
+        if (nt == TT && (p.wide & 32) && valid == 2) write(std::true_type());
+        else write(std::false_type());
         mbar_arrive_warp(&sm.y_empty[yr.slot]);
         yr.next();
       }
