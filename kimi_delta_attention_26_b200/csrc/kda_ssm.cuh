@@ -84,9 +84,42 @@ __device__ __forceinline__ float step_of(float r, int softplus) {
   return fmaf(2.f * s, t, fmaxf(r, 0.f));
 }
 
-// exp2 of a pair; pairs are multiplied and added as one instruction (half the
-// instructions, the same time on the multiply-add pipe)
+// Pairs are multiplied and added as one instruction: half the instructions, the
+// same time on the multiply-add pipe.
+__device__ __forceinline__ float2 pair_of(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 pexp2(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 prcp(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
+
+// sigmoid of a pair; exp(-x) overflows to infinity for x below -88, whose
+// reciprocal is the right 0
+__device__ __forceinline__ float2 psigmoid(float2 x) {
+  return prcp(__fadd2_rn(pair_of(1.f), pexp2(__fmul2_rn(x, pair_of(-kLog2e)))));
+}
+
+// step_of a pair
+template <bool EXACT>
+__device__ __forceinline__ float2 pstep(float2 r, int softplus) {
+  if (!softplus) return r;
+  const float2 m = make_float2(-fabsf(r.x), -fabsf(r.y)), x = __fmul2_rn(m, pair_of(kLog2e));
+  float2 e = pexp2(x);
+  if (EXACT) {
+    const float2 rest = __ffma2_rn(m, pair_of(1.925963033500234e-8f), __ffma2_rn(m, pair_of(kLog2e), make_float2(-x.x, -x.y)));
+    e = __ffma2_rn(__fmul2_rn(e, pair_of(0.6931471805599453f)), rest, e);
+  }
+  const float2 s = __fmul2_rn(e, prcp(__fadd2_rn(pair_of(2.f), e))), w = __fmul2_rn(s, s);
+  float2 t = __ffma2_rn(w, pair_of(1.f / 12), pair_of(1.f / 11));
+  t = __ffma2_rn(w, t, pair_of(1.f / 9));
+  t = __ffma2_rn(w, t, pair_of(1.f / 7));
+  t = __ffma2_rn(w, t, pair_of(1.f / 5));
+  t = __ffma2_rn(w, t, pair_of(1.f / 3));
+  t = __ffma2_rn(w, t, pair_of(1.f));
+  return __ffma2_rn(__fadd2_rn(s, s), t, make_float2(fmaxf(r.x, 0.f), fmaxf(r.y, 0.f)));
+}
 
 // S values at p as pairs (S = 1: the second half is 0)
 template <int S>
@@ -379,22 +412,26 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
           }
         }
         if (t0 + TT < hi) load(t0 + TT, static_cast<int>(min(static_cast<int64_t>(TT), hi - t0 - TT)));
-        float2 v[NU][2];
+        float4 v[NU];
         const bool short_tile = nt < TT || valid < 2;
 #pragma unroll
         for (int k = 0; k < NU; ++k)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float d = step_of<sizeof(T) == 4>(td[k].get(i) + bias[i], p.softplus);
-            v[k][i] = make_float2(d, d * tu[k].get(i));
-            if (short_tile && (tk + k * TK >= nt || i >= valid)) v[k][i] = make_float2(0.f, 0.f);
+        {
+          const float2 r = __fadd2_rn(make_float2(td[k].get(0), td[k].get(1)), make_float2(bias[0], bias[1]));
+          const float2 d = pstep<sizeof(T) == 4>(r, p.softplus);
+          const float2 du = __fmul2_rn(d, make_float2(tu[k].get(0), tu[k].get(1)));
+          v[k] = make_float4(d.x, du.x, d.y, du.y);
+          if (short_tile) {
+            const bool on = tk + k * TK < nt;
+            v[k] = make_float4(on && valid > 0 ? v[k].x : 0.f, on && valid > 0 ? v[k].y : 0.f,
+                               on && valid > 1 ? v[k].z : 0.f, on && valid > 1 ? v[k].w : 0.f);
           }
+        }
         mbar_wait(&sm.empty[to.slot], to.phase);
 #pragma unroll
         for (int k = 0; k < NU; ++k)
           if (TT % TK == 0 || tk + k * TK < TT)
-            *reinterpret_cast<float4*>(&sm.d[to.slot][tk + k * TK][k0]) =
-                make_float4(v[k][0].x, v[k][0].y, v[k][1].x, v[k][1].y);
+            *reinterpret_cast<float4*>(&sm.d[to.slot][tk + k * TK][k0]) = v[k];
 #pragma unroll
         for (int k = 0; k < NB; ++k)
           if (TT * L % ROLE == 0 || tid + k * ROLE < TT * L) {
@@ -440,14 +477,13 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
       if (lo < hi) load(lo, static_cast<int>(min(static_cast<int64_t>(TT), hi - lo)));
       for (int64_t t0 = lo; t0 < hi; t0 += TT) {
         const int nt = static_cast<int>(min(static_cast<int64_t>(TT), hi - t0));
-        float du[4 * NG][2], gate[4 * NG][2];
+        float2 du[4 * NG], gate[4 * NG];
 #pragma unroll
-        for (int k = 0; k < 4 * NG; ++k)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            du[k][i] = p.D ? skip[i] * ru[k].get(i) : 0.f;
-            gate[k][i] = p.z ? silu(rz[k].get(i)) : 1.f;
-          }
+        for (int k = 0; k < 4 * NG; ++k) {
+          const float2 zz = make_float2(rz[k].get(0), rz[k].get(1));
+          du[k] = p.D ? __fmul2_rn(make_float2(skip[0], skip[1]), make_float2(ru[k].get(0), ru[k].get(1))) : pair_of(0.f);
+          gate[k] = p.z ? __fmul2_rn(zz, psigmoid(zz)) : pair_of(1.f);
+        }
         if (t0 + TT < hi) load(t0 + TT, static_cast<int>(min(static_cast<int64_t>(TT), hi - t0 - TT)));
         mbar_wait(&sm.y_full[yr.slot], yr.phase);
         // whole: a full tile of full pairs, nothing to check
@@ -476,7 +512,8 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int k = g * 4 + j;
-              const float y[2] = {(ev[j] + du[k][0]) * gate[k][0], (od[j] + du[k][1]) * gate[k][1]};
+              const float2 v = __fmul2_rn(__fadd2_rn(make_float2(ev[j], od[j]), du[k]), gate[k]);
+              const float y[2] = {v.x, v.y};
               T* to = row + j * p.o_st;
               if (whole.value) {
                 store_f32<T, 2>(to, y);
@@ -651,6 +688,7 @@ struct BwdShared {
   alignas(16) float b[TB][FB][4 * L], c[TB][FB][4 * L];
   alignas(16) unsigned char sum[3][TB / 4][L][QS];  // sum_n g B, sum_n w A, sum_n C h by threads
   float db[WARPS][TB][4 * L], dc[WARPS][TB][4 * L];
+  float4 da[THREADS];          // each thread's sum for dA over the tiles (its own; not in registers, for want of them)
 };
 
 // The sequence backwards, a tile at a time: from the kept states its states and
@@ -684,7 +722,7 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
   const int64_t cn = static_cast<int64_t>(p.C) * p.N;
   const int ch = c0 + chl;
   const bool live = ch < c_end;
-  float2 a[2], g[2], da[2];
+  float2 a[2], g[2];
   {
     float av[4], gv[4];
 #pragma unroll
@@ -699,9 +737,9 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
     for (int i = 0; i < 2; ++i) {
       a[i] = make_float2(av[2 * i], av[2 * i + 1]);
       g[i] = make_float2(gv[2 * i], gv[2 * i + 1]);
-      da[i] = make_float2(0.f, 0.f);
     }
   }
+  sm.da[tid] = make_float4(0.f, 0.f, 0.f, 0.f);
   unsigned char* const sum_row = &sm.sum[0][0][q][chl % 2 * Sh::ODD + chl / 2 * 16];
   constexpr int SUM = TB / 4 * L * Sh::QS;  // bytes between the kinds of sums
   // this thread's part of a tile before and after the states: a channel pair's TG tokens
@@ -905,11 +943,8 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      da[i].x += da_tile[i].x;
-      da[i].y += da_tile[i].y;
-    }
+    const float4 da = sm.da[tid];
+    sm.da[tid] = make_float4(da.x + da_tile[0].x, da.y + da_tile[0].y, da.z + da_tile[1].x, da.w + da_tile[1].y);
     __syncthreads();
     // ------------------------------------------------------- the gradients
     if (k > 0) load_tile(k - 1);
@@ -960,7 +995,8 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
     }
     __syncthreads();
   }
-  const float dv[4] = {da[0].x, da[0].y, da[1].x, da[1].y}, gv[4] = {g[0].x, g[0].y, g[1].x, g[1].y};
+  const float4 da = sm.da[tid];
+  const float dv[4] = {da.x, da.y, da.z, da.w}, gv[4] = {g[0].x, g[0].y, g[1].x, g[1].y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = q * 4 + (i ^ f);
