@@ -449,8 +449,8 @@ kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const
  *   dB, dC          [T, G, S] of u's type (sums over a group's channels)
  *   dA              fp32 [C, S]; dD, ddt_bias fp32 [C] or NULL (not written)
  *   dinitial_state  fp32 [N, C, S] or NULL (not written)
- * All written in full. Scratch from the pool: a state every 16 tokens and the
- * partial sums of dB and dC.
+ * All written in full. Scratch from the pool: a state every 8 tokens (C S / 2
+ * bytes a token) and the partial sums of dB and dC.
  */
 kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
                          const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,

@@ -369,11 +369,15 @@ def _pack(t: Optional[torch.Tensor], name: str, index: int):
     return _desc(t.data_ptr(), n, code, *t.shape, *pad, *t.stride(), *pad)
 
 
-def _device_of(t: torch.Tensor, name: str, dims: int, fn: str) -> int:
+def _dims(t: torch.Tensor, name: str, dims: int) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
+
+
+def _device_of(t: torch.Tensor, name: str, dims: int, fn: str) -> int:
+    _dims(t, name, dims)
     if not t.is_cuda:
         raise ValueError(f"{fn} runs on CUDA tensors only")
     return t.get_device()
@@ -426,7 +430,7 @@ _HERE = _Here()
 
 
 def _on(index: int, stream: Optional[torch.cuda.Stream], tensors):
-    if stream is not None:
+    if stream is not None and (stream.device_index != index or stream != torch.cuda.current_stream(index)):
         return _On(index, stream, tensors)
     return _HERE if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
 
@@ -438,10 +442,11 @@ def _rows_like(t: torch.Tensor) -> torch.Tensor:
 
 def _raise(code: int, checks) -> None:
     """The error of a refused call: what is wrong with a tensor, where the checks find it, else the status."""
+    error = KDAError(code)
     for t, name, dtype, shape, contiguous in checks:
         if t is not None:
             _check(t, name, dtype, shape, t.device, contiguous)
-    raise KDAError(code)
+    raise error
 
 
 def _activation(name: Optional[str]) -> int:
@@ -468,8 +473,7 @@ def kda_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     act = _activation(activation)
     cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
-    if weight.dim() != 2:
-        raise ValueError("weight must be [C, W]")
+    _dims(weight, "weight", 2)
     (T, C), W = x.shape, weight.shape[1]
     with _on(dev, stream, (x, weight, bias, cu_seqlens, initial_state, out, final_state)):
         if out is None:
@@ -498,6 +502,8 @@ def kda_conv_decode(x: torch.Tensor, weight: torch.Tensor, state: torch.Tensor, 
     """
     dev = _device_of(x, "x", 2, "kda_conv_decode")
     act = _activation(activation)
+    _dims(weight, "weight", 2)
+    _dims(state, "state", 3)
     B, C = x.shape
     idx = _int32_ptr(state_indices, "state_indices", dev, B)
     with _on(dev, stream, (x, weight, bias, state, state_indices, out)):
@@ -525,8 +531,7 @@ def kda_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bias
     act = _activation(activation)
     cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
-    if weight.dim() != 2:
-        raise ValueError("weight must be [C, W]")
+    _dims(weight, "weight", 2)
     (T, C), W = x.shape, weight.shape[1]
     with _on(dev, stream, (x, weight, bias, cu_seqlens, initial_state, dout, dfinal_state)):
         dx = _rows_like(x)
@@ -548,7 +553,7 @@ def kda_conv_bwd(x: torch.Tensor, weight: torch.Tensor, dout: torch.Tensor, bias
 
 def _ssm_checks(u, dt, A, B, C, D, z, dt_bias):
     t, (T, c) = u.dtype, u.shape
-    n, g = A.shape[-1], B.shape[1] if B.dim() == 3 else 1
+    n, g = A.shape[1], B.shape[1]
     return [(dt, "dt", t, (T, c), False), (A, "A", torch.float32, (c, n), True), (B, "B", t, (T, g, n), False),
             (C, "C", t, (T, g, n), False), (D, "D", torch.float32, (c,), True), (z, "z", t, (T, c), False),
             (dt_bias, "dt_bias", torch.float32, (c,), True)]
@@ -573,19 +578,21 @@ def kda_ssm_fwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Ten
     dev = _device_of(u, "u", 2, "kda_ssm_fwd")
     cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    _dims(A, "A", 2)
+    _dims(B, "B", 3)
     T, c = u.shape
     with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, out, final_state)):
         if out is None:
             out = _rows_like(u)
         if final_state is None and output_final_state:
-            final_state = torch.empty((N, c, A.shape[-1]), dtype=torch.float32, device=u.device)
+            final_state = torch.empty((N, c, A.shape[1]), dtype=torch.float32, device=u.device)
         rc = _lib.kda_ssm_fwd(_pack(u, "u", dev), _pack(dt, "dt", dev), _pack(A, "A", dev), _pack(B, "B", dev),
                               _pack(C, "C", dev), _pack(D, "D", dev), _pack(z, "z", dev),
                               _pack(dt_bias, "dt_bias", dev), bool(dt_softplus), cu, N,
                               _pack(initial_state, "initial_state", dev), _pack(out, "out", dev),
                               _pack(final_state, "final_state", dev), torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
-        state = (N, c, A.shape[-1])
+        state = (N, c, A.shape[1])
         _raise(rc, _ssm_checks(u, dt, A, B, C, D, z, dt_bias) +
                [(initial_state, "initial_state", torch.float32, state, True), (out, "out", u.dtype, (T, c), False),
                 (final_state, "final_state", torch.float32, state, True)])
@@ -604,6 +611,9 @@ def kda_ssm_decode(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     int32 [R] on the device (distinct slots), or None for slot r.
     """
     dev = _device_of(u, "u", 2, "kda_ssm_decode")
+    _dims(A, "A", 2)
+    _dims(B, "B", 3)
+    _dims(state, "state", 3)
     R, c = u.shape
     idx = _int32_ptr(state_indices, "state_indices", dev, R)
     with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, state, state_indices, out)):
@@ -615,7 +625,7 @@ def kda_ssm_decode(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
                                  _pack(out, "out", dev), torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         _raise(rc, _ssm_checks(u, dt, A, B, C, D, z, dt_bias) +
-               [(state, "state", torch.float32, (state.shape[0], c, A.shape[-1]), True),
+               [(state, "state", torch.float32, (state.shape[0], c, A.shape[1]), True),
                 (out, "out", u.dtype, (R, c), False)])
     return out
 
@@ -634,8 +644,8 @@ def kda_ssm_bwd(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Ten
     cu = _int32_ptr(cu_seqlens, "cu_seqlens", dev)
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
     (T, c), f32 = u.shape, torch.float32
-    if A.dim() != 2 or B.dim() != 3:
-        raise ValueError("A must be [C, S] and B [T, G, S]")
+    _dims(A, "A", 2)
+    _dims(B, "B", 3)
     with _on(dev, stream, (u, dt, A, B, C, D, z, dt_bias, cu_seqlens, initial_state, dout, dfinal_state)):
         def new(shape, dtype=u.dtype, of=u):
             return None if of is None else torch.empty(shape, dtype=dtype, device=u.device)

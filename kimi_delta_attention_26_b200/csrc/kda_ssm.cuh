@@ -68,7 +68,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <bool EXACT>
 __device__ __forceinline__ float step_of(float r, int softplus) {
   if (!softplus) return r;
-  const float m = -fabsf(r), x = m * kLog2e;
+  float m = -fabsf(r);
+  if (EXACT && m < -200.f) m = -200.f;  // e is 0 there; an infinity would make `rest` NaN
+  const float x = m * kLog2e;
   float e = exp2_approx(x);
   if (EXACT) {
     const float rest = fmaf(m, kLog2e, -x) + m * 1.925963033500234e-8f;  // log2(e) less its nearest fp32
@@ -105,7 +107,12 @@ __device__ __forceinline__ float2 psigmoid(float2 x) {
 template <bool EXACT>
 __device__ __forceinline__ float2 pstep(float2 r, int softplus) {
   if (!softplus) return r;
-  const float2 m = make_float2(-fabsf(r.x), -fabsf(r.y)), x = __fmul2_rn(m, pair_of(kLog2e));
+  float2 m = make_float2(-fabsf(r.x), -fabsf(r.y));
+  if (EXACT) {
+    if (m.x < -200.f) m.x = -200.f;
+    if (m.y < -200.f) m.y = -200.f;
+  }
+  const float2 x = __fmul2_rn(m, pair_of(kLog2e));
   float2 e = pexp2(x);
   if (EXACT) {
     const float2 rest = __ffma2_rn(m, pair_of(1.925963033500234e-8f), __ffma2_rn(m, pair_of(kLog2e), make_float2(-x.x, -x.y)));
@@ -119,6 +126,42 @@ __device__ __forceinline__ float2 pstep(float2 r, int softplus) {
   t = __ffma2_rn(w, t, pair_of(1.f / 3));
   t = __ffma2_rn(w, t, pair_of(1.f));
   return __ffma2_rn(__fadd2_rn(s, s), t, make_float2(fmaxf(r.x, 0.f), fmaxf(r.y, 0.f)));
+}
+
+// 2^x on the multiply-add pipe: n + f with n the nearest whole number, 2^f by a
+// polynomial fitted for the least largest relative error on [-1/2, 1/2] (2e-9),
+// n added to the exponent. Its error has no bias (below 1e-9 on average).
+__device__ __forceinline__ float exp2_poly(float x) {
+  const float c = x < -126.f ? -126.f : x > 128.f ? 128.f : x;  // NaN passes
+  const float shifted = c + 12582912.f, f = c - (shifted - 12582912.f);  // 1.5 * 2^23: n in the low bits
+  float t = fmaf(f, 1.5353362e-4f, 1.3398875e-3f);
+  t = fmaf(f, t, 9.6184369e-3f);
+  t = fmaf(f, t, 5.5503324e-2f);
+  t = fmaf(f, t, 2.4022648e-1f);
+  t = fmaf(f, t, 6.9314718e-1f);
+  t = fmaf(f, t, 1.f);
+  const float y = __int_as_float(__float_as_int(t) + (__float_as_int(shifted) << 23));
+  return x == x ? y : x;
+}
+
+// The decay 2^(d a) of a token for two states. ex2.approx is low by 2e-8 on
+// average (measured, 5e-9 to 3e-8 for exponents between -1 and 0), which a state
+// that lasts n tokens takes n times; 1.5e-8 on the exponent, which the
+// multiply-add brings for nothing, halves that. EXACT (fp32 tensors): without
+// it, by the polynomial.
+template <bool EXACT>
+__device__ __forceinline__ float2 pdecay(float2 d, float2 a) {
+  if constexpr (EXACT) {
+    const float2 x = __fmul2_rn(d, a);
+    return make_float2(exp2_poly(x.x), exp2_poly(x.y));
+  } else {
+    return pexp2(__ffma2_rn(d, a, pair_of(1.5e-8f)));
+  }
+}
+
+template <bool EXACT>
+__device__ __forceinline__ float decay(float d, float a) {
+  return EXACT ? exp2_poly(d * a) : exp2_approx(fmaf(d, a, 1.5e-8f));
 }
 
 // S values at p as pairs (S = 1: the second half is 0)
@@ -268,7 +311,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
         if (on && p.run && !split_pass && lo > start) {
           // the state before this range: those of the ranges since the sequence's start, decayed
           for (int64_t r = start / p.run; r < range; ++r)
-            hv[i] = fmaf(r * p.run <= start ? 0.f : exp2_approx(av[i] * p.sum_d[r * p.C + c0 + ch]), hv[i],
+            hv[i] = fmaf(r * p.run <= start ? 0.f : exp2_poly(av[i] * p.sum_d[r * p.C + c0 + ch]), hv[i],
                          p.carry[r * cn + row + i]);
         }
       }
@@ -306,7 +349,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
             const float2 dd = make_float2(d.x, d.x), du = make_float2(d.y, d.y);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-              h[i] = __ffma2_rn(pexp2(__fmul2_rn(dd, a[i])), h[i], __fmul2_rn(du, b[i]));
+              h[i] = __ffma2_rn(pdecay<sizeof(T) == 4>(dd, a[i]), h[i], __fmul2_rn(du, b[i]));
               if (OUT) acc = i ? __ffma2_rn(c[i], h[i], acc) : __fmul2_rn(c[i], h[i]);
             }
             if (OUT) y[j] = S > 1 ? acc.x + acc.y : acc.x;
@@ -553,7 +596,7 @@ struct DecodeParams {
   int64_t u_st, dt_st, z_st, o_st, b_st, b_sg, c_st, c_sg;
   int C, N, G;
   int softplus;
-  int wide;                 // bits 0, 1, 2: rows of B, C, state and A can be moved four states at a time
+  int wide;                 // bits 0, 1, 2: rows of B, C, state and A can be moved four states at a time; 3: four channels, several groups
 };
 
 // One block: 512 / L channels of one request, four channels per group of L
@@ -583,17 +626,17 @@ __global__ void __launch_bounds__(NTHREADS) ssm_decode_kernel(DecodeParams p) {
   const float* A = p.A + static_cast<int64_t>(c0) * p.N + n0;
   if (wide && nv == S && c0 + 4 <= p.C) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_f32<float, S>(h[j], st + static_cast<int64_t>(j) * p.N);
+    for (int j = 0; j < 4; ++j) load_f32<float, S>(h[j], st + j * p.N);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_f32<float, S>(a[j], A + static_cast<int64_t>(j) * p.N);
+    for (int j = 0; j < 4; ++j) load_f32<float, S>(a[j], A + j * p.N);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < S; ++i) {
         const bool on = c0 + j < p.C && i < nv;
-        h[j][i] = on ? st[static_cast<int64_t>(j) * p.N + i] : 0.f;
-        a[j][i] = on ? A[static_cast<int64_t>(j) * p.N + i] : 0.f;
+        h[j][i] = on ? st[j * p.N + i] : 0.f;
+        a[j][i] = on ? A[j * p.N + i] : 0.f;
       }
   }
   float uu = 0.f, raw = 0.f, gate = 1.f, skip = 0.f;
@@ -603,8 +646,9 @@ __global__ void __launch_bounds__(NTHREADS) ssm_decode_kernel(DecodeParams p) {
     if (p.z) gate = to_f32(static_cast<const T*>(p.z)[r * p.z_st + mine]);
     if (p.D) skip = p.D[mine];
   }
-  // a group's four channels may belong to different groups of B and C
-  const int cg = p.C / p.G;
+  // the four channels may belong to different groups of B and C
+  const bool several = p.wide & 8;
+  const int cg = p.G > 1 ? p.C / p.G : p.C;
   float b[S], c[S];
   int group = -1;
   auto load_bc = [&](int g) {
@@ -616,29 +660,29 @@ __global__ void __launch_bounds__(NTHREADS) ssm_decode_kernel(DecodeParams p) {
     vc[0].get(c);
     group = g;
   };
-  load_bc(min(c0, p.C - 1) / cg);
+  load_bc(p.G > 1 ? min(c0, p.C - 1) / cg : 0);
   const float d = step_of<sizeof(T) == 4>(raw, p.softplus), du = d * uu;
   float y[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float dj = __shfl_sync(ALL, d, j, L), uj = __shfl_sync(ALL, du, j, L);
-    if (j && c0 + j < p.C && (c0 + j) / cg != group) load_bc((c0 + j) / cg);
+    if (several && j && c0 + j < p.C && (c0 + j) / cg != group) load_bc((c0 + j) / cg);
     y[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      h[j][i] = fmaf(exp2_approx(dj * (a[j][i] * kLog2e)), h[j][i], uj * b[i]);
+      h[j][i] = fmaf(decay<sizeof(T) == 4>(dj, a[j][i] * kLog2e), h[j][i], uj * b[i]);
       y[j] = fmaf(c[i], h[j][i], y[j]);
     }
   }
   if (wide && nv == S && c0 + 4 <= p.C) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) store_f32<float, S>(st + static_cast<int64_t>(j) * p.N, h[j]);
+    for (int j = 0; j < 4; ++j) store_f32<float, S>(st + j * p.N, h[j]);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < S; ++i)
-        if (c0 + j < p.C && i < nv) st[static_cast<int64_t>(j) * p.N + i] = h[j][i];
+        if (c0 + j < p.C && i < nv) st[j * p.N + i] = h[j][i];
   }
   // over the group's threads: thread q ends with channel q % 4
   const bool up2 = q & 2, up1 = q & 1;
@@ -868,7 +912,7 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
         const float2 dd = make_float2(d.x, d.x), du = make_float2(d.y, d.y);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          e[t][i] = pexp2(__fmul2_rn(dd, a[i]));
+          e[t][i] = pdecay<sizeof(T) == 4>(dd, a[i]);
           h[t][i] = __ffma2_rn(e[t][i], t ? h[t - 1][i] : h0[i], __fmul2_rn(du, b[i]));
         }
         if (p.z) {

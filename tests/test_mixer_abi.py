@@ -210,3 +210,5 @@ def test_binding_refuses_cpu_tensors_and_bad_names():
             f()
     with pytest.raises(TypeError):
         kda.kda_conv_fwd([1], w)
+    with pytest.raises(ValueError):
+        kda.kda_conv_fwd(x[0], w)

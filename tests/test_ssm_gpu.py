@@ -194,6 +194,36 @@ def test_scan_extreme_steps(kda):
     check_all(kda, d, [50], large_steps=True)
 
 
+@pytest.mark.parametrize("typ", list(TYPES))
+def test_scan_masked_steps(kda, typ):
+    """A step masked by the type's lowest value or by minus infinity before the
+    softplus is 0: the token leaves the state as it is (whatever u, B and C hold,
+    as long as they are finite) and gets no gradient through it; plus infinity
+    forgets the state, NaN stays in its channel."""
+    dtype = TYPES[typ]
+    d = make([40], 24, 16, 1, dtype, seed=61)
+    keep = [t for t in range(40) if t not in (5, 6, 20)]
+    d["dt"][5], d["dt"][6], d["dt"][20] = torch.finfo(dtype).min, float("-inf"), torch.finfo(dtype).min
+    out, fin = fwd(kda, d, initial_state=d["init"])
+    e = {k: (v[keep].contiguous() if k in ("u", "dt", "B", "C", "z", "dout") else v) for k, v in d.items()}
+    ref, rfin = fwd(kda, e, initial_state=d["init"])
+    assert torch.equal(out[keep], ref) and torch.equal(fin, rfin)
+    assert bool(torch.isfinite(out).all())
+    gr = bwd(kda, d, initial_state=d["init"], dfinal_state=d["dfin"])
+    for k, v in gr.items():
+        assert bool(torch.isfinite(v).all()), k
+    assert not bool(gr["ddt"][[5, 6, 20]].any())
+    state = d["init"].clone()
+    r = slice(6, 7)
+    kda.kda_ssm_decode(d["u"][r], d["dt"][r], d["A"], d["B"][r], d["C"][r], state, d["D"], d["z"][r], d["bias"])
+    assert torch.equal(state, d["init"])
+    d["dt"][10, 3] = float("nan")
+    out2, _ = fwd(kda, d, initial_state=d["init"])
+    same = torch.ones_like(out, dtype=torch.bool)
+    same[10:, 3] = False
+    assert torch.equal(out2[same], out[same]) and bool(out2[10:, 3].isnan().all())
+
+
 @pytest.mark.parametrize("n,G", [(16, 1), (5, 3), (128, 1)])
 def test_scan_pieces_and_tokens(kda, n, G):
     """A prompt in two pieces and then token by token agrees with the whole
