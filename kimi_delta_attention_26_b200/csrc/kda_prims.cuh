@@ -1,6 +1,6 @@
 // kda_prims.cuh -- PTX wrappers shared by the library's kernels: mbarriers
 // (bounded waits), TMA tensor and bulk copies, cluster signalling, ldmatrix,
-// mma.sync and conversions. Included by each translation unit, which has its own
+// mma.sync and conversions. Each translation unit that includes it has its own
 // status words.
 #pragma once
 
@@ -24,11 +24,11 @@ constexpr long long kWaitCycles = 1ll << 28;  // ~0.14 s at 1.9 GHz
 // A waiting thread is suspended in hardware (up to this many ns per try)
 // instead of spinning, so waiting warps leave the issue slots to the others.
 constexpr uint32_t kSuspendHintNs = 20000;
-static __device__ unsigned int g_wait_timeouts = 0;
+__device__ unsigned int g_wait_timeouts = 0;
 
 // Device status word (bit 0: a cu_seqlens that is not a non-decreasing
 // partition of [0, T)); read and cleared through the C ABI.
-static __device__ unsigned int g_device_flags = 0;
+__device__ unsigned int g_device_flags = 0;
 constexpr unsigned int kFlagBadCuSeqlens = 1u;
 
 // Checks sequence `seq`'s boundaries of a packed batch of `nseq` sequences
