@@ -95,6 +95,39 @@ __device__ __forceinline__ void fma_to(float (&acc)[V], const float (&x)[V], con
   }
 }
 
+// the activation of a row, and dp = dy act'(a)
+template <int V>
+__device__ __forceinline__ void activate(float (&a)[V], int act) {
+  if (!act) return;
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 y = psilu(make_float2(a[i], a[i + 1]));
+      a[i] = y.x;
+      a[i + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] = silu(a[i]);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void pre_gradient(float (&dp)[V], const float (&dy)[V], const float (&a)[V], int act) {
+  if constexpr (V % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      float2 g = make_float2(dy[i], dy[i + 1]);
+      if (act) g = __fmul2_rn(g, pdsilu(make_float2(a[i], a[i + 1])));
+      dp[i] = g.x;
+      dp[i + 1] = g.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) dp[i] = act ? dy[i] * dsilu(a[i]) : dy[i];
+  }
+}
+
 constexpr int KT = 4;  // tokens loaded together; the last inputs are a ring of KT rows, row t % KT
 
 template <typename T, int V, int W>
@@ -155,10 +188,7 @@ __global__ void __launch_bounds__(NTHREADS) conv_fwd_kernel(Params p) {
       for (int i = 0; i < V; ++i) a[i] = b[i];
 #pragma unroll
       for (int j = 0; j < W; ++j) fma_to<V>(a, w[j], ring[(k + KT - (W - 1) + j) % KT]);
-      if (p.silu) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = silu(a[i]);
-      }
+      activate<V>(a, p.silu);
       store_f32<T, V>(out + k * p.o_st, a);
     };
     fetch();
@@ -240,10 +270,7 @@ __global__ void __launch_bounds__(NTHREADS) conv_decode_kernel(DecodeParams p) {
       raw[j].get(x);
       fma_to<V>(y, w[j], x);
     }
-    if (p.silu) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = silu(y[i]);
-    }
+    activate<V>(y, p.silu);
     store_f32<T, V>(static_cast<T*>(p.out) + b * p.o_st + c, y);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) raw[j + 1].store(st + j * p.C);
@@ -267,13 +294,6 @@ struct BwdParams {
   int N;
   int silu;
 };
-
-// dp at a token with the activation's input a
-template <int V>
-__device__ __forceinline__ void pre_gradient(float (&dp)[V], const float (&dy)[V], const float (&a)[V], int act) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) dp[i] = act ? dy[i] * dsilu(a[i]) : dy[i];
-}
 
 // A warp walks its run of tokens forwards: at token t it has the inputs
 // t - W + 1 .. t and the last W - 1 values of dp, so dx_{t-W+1} is complete. It

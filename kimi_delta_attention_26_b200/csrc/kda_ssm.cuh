@@ -51,14 +51,6 @@ struct Params {
   int wide;                 // bits 0..5: rows of u, dt, z, B, C, out can be moved in pieces (u, dt, z, out: 2; B, C: S)
 };
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-
 // The step: log(1 + exp(r)) = max(r, 0) + log1p(e) with e = exp(-|r|) in (0, 1],
 // and log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3. atanh(s) / s as a
 // polynomial in w = s^2 <= 1/9, of degree 6: its series to w^5 / 11 with the
@@ -84,23 +76,6 @@ __device__ __forceinline__ float step_of(float r, int softplus) {
   t = fmaf(w, t, 1.f / 3);
   t = fmaf(w, t, 1.f);
   return fmaf(2.f * s, t, fmaxf(r, 0.f));
-}
-
-// Pairs are multiplied and added as one instruction: half the instructions, the
-// same time on the multiply-add pipe.
-__device__ __forceinline__ float2 pair_of(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 pexp2(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float2 prcp(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
-
-// sigmoid of a pair; exp(-x) overflows to infinity for x below -88, whose
-// reciprocal is the right 0
-__device__ __forceinline__ float2 psigmoid(float2 x) {
-  return prcp(__fadd2_rn(pair_of(1.f), pexp2(__fmul2_rn(x, pair_of(-kLog2e)))));
 }
 
 // step_of a pair
