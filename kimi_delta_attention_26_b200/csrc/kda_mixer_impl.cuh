@@ -78,7 +78,7 @@ cudaError_t Mixer<T>::scan(ssm::Params p, bool out, int ranges, int sms, cudaStr
     p.blocks_per_group = (p.C / p.G + CH - 1) / CH;
     const int64_t blocks = static_cast<int64_t>(p.G) * p.blocks_per_group;
     auto go = [&](auto o, auto deep) {
-      using Sh = ssm::FwdShared<T, l.value, s.value, CH, deep.value>;
+      using Sh = ssm::FwdShared<T, l.value, s.value, CH, o.value, deep.value>;
       auto* kernel = ssm::ssm_fwd_kernel<T, l.value, s.value, CH, o.value, deep.value>;
       if ((e = allow_shared(kernel, sizeof(Sh))) == cudaSuccess)
         kernel<<<dim3(static_cast<unsigned>(blocks), ranges), Sh::THREADS, sizeof(Sh), stream>>>(p);

@@ -199,18 +199,18 @@ constexpr int ROLE = NTHREADS;              // threads that make tiles; as many 
 // Two shapes of the forward scan. DEEP: one block per SM, longer tiles and more
 // straight-line code, for grids that give an SM no second block; else two
 // blocks per SM share it.
-template <typename T, int L, int S, int CH, bool DEEP>
+template <typename T, int L, int S, int CH, bool OUT, bool DEEP>
 struct FwdShared {
   static constexpr int TT = DEEP ? 64 : 32;  // tokens per tile
   static constexpr int GT = DEEP ? 16 : 8;   // tokens of straight-line code in the states' loop
-  static constexpr int STATE_THREADS = CH * L, THREADS = STATE_THREADS + 2 * ROLE;
+  static constexpr int STATE_THREADS = CH * L, THREADS = STATE_THREADS + (OUT ? 2 : 1) * ROLE;
   // The parts of the outputs: 16 bytes (four tokens) per thread and four
   // tokens, even channels before odd ones. The strides put the eight threads
   // of a store and of a load into different banks.
   static constexpr int ODD = CH / 2 * 16 + 64, QS = 2 * ODD + 16;
   float2 d[STAGES][TT][CH];        // d, d u
-  alignas(16) float b[STAGES][TT][L * S], c[STAGES][TT][L * S];
-  alignas(16) unsigned char y[YSLOTS][TT / 4][L][QS];
+  alignas(16) float b[STAGES][TT][L * S], c[OUT ? STAGES : 1][OUT ? TT : 1][L * S];
+  alignas(16) unsigned char y[YSLOTS][OUT ? TT / 4 : 1][L][QS];
   unsigned long long full[STAGES], empty[STAGES], y_full[YSLOTS], y_empty[YSLOTS];
 };
 
@@ -234,8 +234,9 @@ struct Ring {
 // of STAGES) and the outputs (D u, the gate).
 // OUT: the outputs; else states only, for the gradients (ck) or the time split (carry).
 template <typename T, int L, int S, int CH, bool OUT, bool DEEP>
-__global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP || L >= 16 ? 1 : 2) ssm_fwd_kernel(Params p) {
-  using Sh = FwdShared<T, L, S, CH, DEEP>;
+__global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DEEP || L >= 16 ? 1 : OUT ? 2 : 3)
+    ssm_fwd_kernel(Params p) {
+  using Sh = FwdShared<T, L, S, CH, OUT, DEEP>;
   constexpr int SN = Sh::STATE_THREADS, TT = Sh::TT, GT = OUT ? Sh::GT : KT;
   extern __shared__ __align__(16) unsigned char smem[];
   Sh& sm = *reinterpret_cast<Sh*>(smem);
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, DEEP>::THREADS, DEEP ||
         if (OUT) mbar_wait(&sm.y_empty[yr.slot], yr.phase);
         const float2* dp = &sm.d[in.slot][0][ch];
         const float* bp = &sm.b[in.slot][0][q * S];
-        const float* cp = &sm.c[in.slot][0][q * S];
+        const float* cp = &sm.c[OUT ? in.slot : 0][0][q * S];
         unsigned char* yp = &sm.y[yr.slot][0][q][ch % 2 * Sh::ODD + ch / 2 * 16];
         for (int t = 0; t < nt; t += GT, dp += GT * CH, bp += GT * L * S, cp += GT * L * S, yp += GT / 4 * L * Sh::QS) {
           if (!OUT && p.ck && live) {  // the state before token t, for the gradients
