@@ -1085,7 +1085,8 @@ __global__ void __launch_bounds__(256) ssm_reduce_kernel(ReduceParams p) {
     const int g = static_cast<int>(i % gn / p.N), n = static_cast<int>(i % p.N);
     float vb = 0.f, vc = 0.f;
     if (t >= lo && t < hi) {
-      for (int k = 0; k < p.blocks_per_group; ++k) {
+#pragma unroll 16
+      for (int k = 0; k < p.blocks_per_group; ++k) {  // loads in flight
         const int64_t at = (static_cast<int64_t>(g * p.blocks_per_group + k) * p.T + t) * p.N + n;
         vb += p.part_b[at];
         vc += p.part_c[at];
