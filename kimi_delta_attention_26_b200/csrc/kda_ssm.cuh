@@ -59,6 +59,11 @@ struct Params {
   int wide;                 // bits 0..5: rows of u, dt, z, B, C, out can be moved in pieces (u, dt, z, out: 2; B, C: S)
 };
 
+// log2(e) less its nearest fp32: the second part of a constant in two parts (the
+// argument reduction of Cody and Waite)
+constexpr float kLog2eRest = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
+constexpr float kLn2 = 0.69314718055994530942f;
+
 // The step: log(1 + exp(r)) = max(r, 0) + log1p(e) with e = exp(-|r|) in (0, 1],
 // and log1p(e) = 2 atanh(s) with s = e / (2 + e) <= 1/3. atanh(s) / s as a
 // polynomial in w = s^2 <= 1/9, of degree 6: its series to w^5 / 11 with the
@@ -73,8 +78,8 @@ __device__ __forceinline__ float step_of(float r, int softplus) {
   const float x = m * kLog2e;
   float e = exp2_approx(x);
   if (EXACT) {
-    const float rest = fmaf(m, kLog2e, -x) + m * 1.925963033500234e-8f;  // log2(e) less its nearest fp32
-    e = fmaf(e * 0.6931471805599453f, rest, e);
+    const float rest = fmaf(m, kLog2e, -x) + m * kLog2eRest;
+    e = fmaf(e * kLn2, rest, e);
   }
   const float s = __fdividef(e, 2.f + e), w = s * s;
   float t = fmaf(w, 1.f / 12, 1.f / 11);
@@ -98,8 +103,8 @@ __device__ __forceinline__ float2 pstep(float2 r, int softplus) {
   const float2 x = __fmul2_rn(m, pair_of(kLog2e));
   float2 e = pexp2(x);
   if (EXACT) {
-    const float2 rest = __ffma2_rn(m, pair_of(1.925963033500234e-8f), __ffma2_rn(m, pair_of(kLog2e), make_float2(-x.x, -x.y)));
-    e = __ffma2_rn(__fmul2_rn(e, pair_of(0.6931471805599453f)), rest, e);
+    const float2 rest = __ffma2_rn(m, pair_of(kLog2eRest), __ffma2_rn(m, pair_of(kLog2e), make_float2(-x.x, -x.y)));
+    e = __ffma2_rn(__fmul2_rn(e, pair_of(kLn2)), rest, e);
   }
   const float2 s = __fmul2_rn(e, prcp(__fadd2_rn(pair_of(2.f), e))), w = __fmul2_rn(s, s);
   float2 t = __ffma2_rn(w, pair_of(1.f / 12), pair_of(1.f / 11));
@@ -111,9 +116,11 @@ __device__ __forceinline__ float2 pstep(float2 r, int softplus) {
   return __ffma2_rn(__fadd2_rn(s, s), t, make_float2(fmaxf(r.x, 0.f), fmaxf(r.y, 0.f)));
 }
 
-// 2^x on the multiply-add pipe: n + f with n the nearest whole number, 2^f by a
-// polynomial fitted for the least largest relative error on [-1/2, 1/2] (2e-9),
-// n added to the exponent. Its error has no bias (below 1e-9 on average).
+// 2^x on the multiply-add pipe: x = n + f with n the nearest whole number (Cody
+// and Waite), 2^f by a polynomial of degree 6 fitted by reweighted least squares
+// (Lawson) for the least largest relative error on [-1/2, 1/2], 2e-9, n added to
+// the exponent. In fp32 it is at most 8e-8 off, 3e-8 in the mean square, and
+// without bias (1e-9 on average).
 __device__ __forceinline__ float exp2_poly(float x) {
   const float c = x < -126.f ? -126.f : x > 128.f ? 128.f : x;  // NaN passes
   const float shifted = c + 12582912.f, f = c - (shifted - 12582912.f);  // 1.5 * 2^23: n in the low bits
@@ -448,8 +455,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
         float4 v[NU];
         const bool short_tile = nt < TT || valid < 2;
 #pragma unroll
-        for (int k = 0; k < NU; ++k)
-        {
+        for (int k = 0; k < NU; ++k) {
           const float2 r = __fadd2_rn(make_float2(td[k].get(0), td[k].get(1)), make_float2(bias[0], bias[1]));
           const float2 d = pstep<sizeof(T) == 4>(r, p.softplus);
           const float2 du = __fmul2_rn(d, make_float2(tu[k].get(0), tu[k].get(1)));
@@ -1023,7 +1029,7 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
         if (t >= nt || c0 + xc >= c_end) continue;
         const float2 d = sm.d[t][xc];
         const float dy = sm.dy[t][xc], uu = (&sm.u[t][0].x)[xc];
-        const float dd = (&sm.sig[t][0].x)[xc] * fmaf(uu, s[0][j], s[1][j] * 0.6931471805599453f);  // A came times log2(e)
+        const float dd = (&sm.sig[t][0].x)[xc] * fmaf(uu, s[0][j], s[1][j] * kLn2);  // A came times log2(e)
         sum_bias += dd;
         sum_d = fmaf(dy, uu, sum_d);
         gd[j * bp.ddt_st] = from_f32<T>(dd);

@@ -1,5 +1,9 @@
 """The 64-bit references of the convolution and the scan against differences of
 their own forward (CPU): a wrong formula there would hide one in a kernel."""
+import os
+import re
+
+import numpy as np
 import pytest
 import torch
 
@@ -56,3 +60,33 @@ def test_scan_gradients(softplus, gate):
              ("init", "dinitial_state")] + ([("z", "dz")] if gate else [])
     for wrt, name in names:
         _differences(loss, a, wrt, gr[name])
+
+
+def test_polynomials_of_the_scan():
+    """The two polynomials in the scan's source, evaluated in fp32 with one rounding
+    a step: 2^f on [-1/2, 1/2] and atanh(s) / s for the softplus, against 64 bits.
+    The bounds are those that the source states, plus fp32's half steps (six
+    and eight of 2^-24 at most, most of them far from the last one)."""
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kimi_delta_attention_26_b200",
+                            "csrc", "kda_ssm.cuh")).read()
+    body = src[src.index("float exp2_poly(float x)"):]
+    body = body[:body.index("const float y")]
+    first = re.search(r"fmaf\(f, ([-\d.e]+)f, ([-\d.e]+)f\)", body)
+    c = [float(first.group(1)), float(first.group(2))] + [float(x) for x in re.findall(r"fmaf\(f, t, ([-\d.e]+)f\)", body)]
+    assert len(c) == 7 and c[-1] == 1.0
+    f = np.linspace(-0.5, 0.5, 100001).astype(np.float32)
+    t = np.full_like(f, np.float32(c[0]))
+    for k in c[1:]:  # a multiply-add rounds once: exact in 64 bits, then to fp32
+        t = (t.astype(np.float64) * f + np.float64(np.float32(k))).astype(np.float32)
+    err = t / np.exp2(f.astype(np.float64)) - 1
+    assert np.abs(err).max() <= 1e-7 and abs(err.mean()) <= 2e-9
+    exact = np.polyval(c, f.astype(np.float64)) / np.exp2(f.astype(np.float64)) - 1
+    assert np.abs(exact).max() <= 3e-8  # the coefficients' own rounding to fp32 on top of 2e-9
+    body = src[src.index("float step_of(float r"):]
+    body = body[:body.index("return fmaf(2.f * s")]
+    head = re.search(r"fmaf\(w, 1\.f / (\d+), 1\.f / (\d+)\)", body)
+    c = [1 / int(head.group(1)), 1 / int(head.group(2))] + [1 / int(x) for x in re.findall(r"fmaf\(w, t, 1\.f / (\d+)\)", body)] + [1.0]
+    assert c[1:] == [1 / 11, 1 / 9, 1 / 7, 1 / 5, 1 / 3, 1.0]
+    e = np.linspace(1e-4, 1, 100001)
+    s = e / (2 + e)
+    assert np.abs(2 * s * np.polyval(c, s * s) / np.log1p(e) - 1).max() <= 2.0 ** -26
