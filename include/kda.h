@@ -262,6 +262,8 @@ kda_status_t kda_set_schedule(int32_t mode, int32_t clusters);
  *   mode 0 (default): split when num_seqs = 1, T >= 4096 and the device holds
  *                     all 3 * H clusters of the three launches at once;
  *   mode 1: never;   mode 2: whenever num_seqs = 1 and T >= 32 (testing).
+ * kda_ssm_fwd and kda_ssm_bwd have a time split of their own under the same
+ * modes; see there.
  * kda_fwd_noalloc never splits. Process-wide. Returns KDA_ERR_SHAPE for any
  * other mode (the setting is then unchanged).
  */
@@ -450,7 +452,8 @@ kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const
  *   dA              fp32 [C, S]; dD, ddt_bias fp32 [C] or NULL (not written)
  *   dinitial_state  fp32 [N, C, S] or NULL (not written)
  * All written in full. Scratch from the pool: a state every 8 tokens (C S / 2
- * bytes a token) and the partial sums of dB and dC.
+ * bytes a token) and the partial sums of dB and dC. The time split applies as
+ * for kda_ssm_fwd, from more channels and fewer tokens on.
  */
 kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
                          const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,

@@ -138,8 +138,9 @@ def set_path(path: int) -> None:
 
 
 def set_time_split(mode: int) -> None:
-    """Time-split prefill of one long sequence (16-token path): 0 automatic
-    (default), 1 never, 2 whenever possible. Process-wide."""
+    """Time-split prefill of one long sequence (16-token path), and the time split
+    of the selective scan and its gradients: 0 automatic (default), 1 never, 2
+    whenever possible. Process-wide."""
     rc = _lib.kda_set_time_split(int(mode))
     if rc != 0:
         raise KDAError(rc)

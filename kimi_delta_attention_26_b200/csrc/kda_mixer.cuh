@@ -14,10 +14,10 @@ struct Mixer {
   static cudaError_t conv_fwd(const conv::Params& p, int W, bool vec, dim3 grid, cudaStream_t stream);
   static cudaError_t conv_decode(const conv::DecodeParams& p, int W, bool vec, dim3 grid, cudaStream_t stream);
   static cudaError_t conv_bwd(const conv::BwdParams& p, int W, bool vec, dim3 grid, cudaStream_t stream);
-  // the forward scan over `ranges` ranges (out: the outputs, else states only) on a device of `sms` SMs
-  static cudaError_t scan(ssm::Params p, bool out, int ranges, int sms, cudaStream_t stream);
+  // a scan over `ranges` ranges (mode: ssm::OUTPUTS, STATES or BACK) on a device of `sms` SMs
+  static cudaError_t scan(ssm::Params p, int mode, int ranges, int sms, cudaStream_t stream);
   static cudaError_t scan_decode(const ssm::DecodeParams& p, int64_t requests, cudaStream_t stream);
-  static cudaError_t scan_bwd(ssm::BwdParams p, cudaStream_t stream);
+  static cudaError_t scan_bwd(ssm::BwdParams p, int ranges, cudaStream_t stream);
   static cudaError_t scan_reduce(const ssm::ReduceParams& p, unsigned blocks, cudaStream_t stream);
   // this translation unit's status words: OR-ed and added to the two words, then cleared where asked
   static cudaError_t status(uint32_t* flags, uint32_t* waits, bool reset_flags, bool reset_waits);

@@ -71,7 +71,7 @@ cudaError_t Mixer<T>::conv_bwd(const conv::BwdParams& p, int W, bool vec, dim3 g
 // channels x 16 states, bf16): one sequence, 128 blocks, 309 us deep and 347 us
 // not; 8 sequences, 1024 blocks, 288 us and 247 us.
 template <typename T>
-cudaError_t Mixer<T>::scan(ssm::Params p, bool out, int ranges, int sms, cudaStream_t stream) {
+cudaError_t Mixer<T>::scan(ssm::Params p, int mode, int ranges, int sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   by_states(p.N, [&](auto l, auto s) {
     constexpr int CH = 128 / l.value;
@@ -84,13 +84,14 @@ cudaError_t Mixer<T>::scan(ssm::Params p, bool out, int ranges, int sms, cudaStr
         kernel<<<dim3(static_cast<unsigned>(blocks), ranges), Sh::THREADS, sizeof(Sh), stream>>>(p);
     };
     auto shape = [&](auto o) {
-      if constexpr (s.value == 4 && l.value <= 8) {
+      if constexpr (s.value == 4 && l.value <= 8 && o.value != ssm::BACK) {
         if (blocks * ranges <= sms) return go(o, std::true_type());
       }
       go(o, std::false_type());
     };
-    if (out) shape(std::true_type());
-    else shape(std::false_type());
+    if (mode == ssm::OUTPUTS) shape(Int<ssm::OUTPUTS>());
+    else if (mode == ssm::STATES) shape(Int<ssm::STATES>());
+    else shape(Int<ssm::BACK>());
   });
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -106,13 +107,17 @@ cudaError_t Mixer<T>::scan_decode(const ssm::DecodeParams& p, int64_t requests, 
 }
 
 template <typename T>
-cudaError_t Mixer<T>::scan_bwd(ssm::BwdParams p, cudaStream_t stream) {
+cudaError_t Mixer<T>::scan_bwd(ssm::BwdParams p, int ranges, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   by_states(p.f.N, [&](auto l, auto) {
     constexpr size_t bytes = sizeof(ssm::BwdShared<l.value>);
-    auto* kernel = ssm::ssm_bwd_kernel<T, l.value>;
-    if ((e = allow_shared(kernel, bytes)) == cudaSuccess)
-      kernel<<<dim3(p.f.G * p.f.blocks_per_group, p.f.NS), ssm::BwdShared<l.value>::THREADS, bytes, stream>>>(p);
+    auto go = [&](auto split) {
+      auto* kernel = ssm::ssm_bwd_kernel<T, l.value, split.value>;
+      if ((e = allow_shared(kernel, bytes)) == cudaSuccess)
+        kernel<<<dim3(p.f.G * p.f.blocks_per_group, ranges), ssm::BwdShared<l.value>::THREADS, bytes, stream>>>(p);
+    };
+    if (p.f.run) go(std::true_type());
+    else go(std::false_type());
   });
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -49,7 +49,12 @@ struct Params {
   float* fin;               // [NS, C, N] or null
   float* ck;                // states before every KT tokens of a sequence, or null
   float* carry;             // time split: [ranges, C, N] each range's last state, else null
-  float* sum_d;             // and [ranges, C] the sum of its steps
+  float* sum_d;             // and [ranges, C] the sum of that piece's steps
+  // the reverse pass of a time-split gradient
+  const void* dout;
+  const float* dfin;        // [NS, C, N] or null: zeros
+  float* back;              // [ranges, C, N] the states' gradient before each range's first piece
+  int64_t dout_st;
   int64_t T;
   int64_t run;              // time split: tokens per range, else 0 (a range is a sequence)
   int64_t u_st, dt_st, z_st, o_st, b_st, b_sg, c_st, c_sg;  // element strides over tokens and groups
@@ -174,25 +179,30 @@ __device__ __forceinline__ int64_t first_kept(int64_t start, int seq) { return s
 
 // A range's pieces of sequences, in order: f(seq, start, end, lo, hi) for the
 // tokens [lo, hi) of the sequence [start, end). A range is a sequence, or, with
-// the time split, `run` tokens of the packed batch. `last_cut` visits only the
-// piece that goes on in the next range.
+// the time split, `run` tokens of the packed batch (a multiple of BORDER), its
+// borders moved up to the next multiple of BORDER tokens of the sequence that they
+// cut. `which`: all pieces, the one that goes on in the next range, or the one
+// that began in an earlier range.
+constexpr int BORDER = 16;
+enum { ALL_PIECES, GOES_ON, CAME_IN };
+__device__ __forceinline__ int64_t border(int64_t r, int64_t start) {
+  return start + (r - start + BORDER - 1) / BORDER * BORDER;
+}
 template <typename F>
-__device__ __forceinline__ void for_pieces(const Params& p, int range, bool last_cut, F f) {
-  if (!p.run) {
-    const int64_t start = bound(p.cu, range, p.T), end = max(start, bound(p.cu, range + 1, p.T));
-    f(range, start, end, start, end);
-    return;
-  }
+__device__ __forceinline__ void split_pieces(const Params& p, int range, int which, F f) {
   const int64_t r0 = range * p.run, r1 = min(r0 + p.run, p.T);
-  int64_t pos = r0;
-  for (int s = first_sequence(p.cu, p.NS, last_cut ? r1 - 1 : r0); s < p.NS; ++s) {
+  for (int s = first_sequence(p.cu, p.NS, which == GOES_ON ? r1 - 1 : r0); s < p.NS; ++s) {
     const int64_t start = bound(p.cu, s, p.T), end = bound(p.cu, s + 1, p.T);
-    if (start >= r1) break;
-    const int64_t lo = max(start, pos), hi = min(end, r1);
-    if (hi <= lo) continue;
-    pos = hi;
-    if (!last_cut || end > r1) f(s, start, end, lo, hi);
+    if (start >= r1 || (which == CAME_IN && start >= r0)) break;
+    const int64_t lo = start >= r0 ? start : border(r0, start), hi = r1 < p.T ? min(end, border(r1, start)) : end;
+    if (hi > lo && (which != GOES_ON || end > hi)) f(s, start, end, lo, hi);
   }
+}
+template <typename F>
+__device__ __forceinline__ void for_pieces(const Params& p, int range, int which, F f) {
+  if (p.run) return split_pieces(p, range, which, f);
+  const int64_t start = bound(p.cu, range, p.T), end = max(start, bound(p.cu, range + 1, p.T));
+  f(range, start, end, start, end);
 }
 
 // K rows of V elements, the rows base + row(k) * st. `all`: one access each; else
@@ -211,11 +221,16 @@ __device__ __forceinline__ void load_rows(Vec<T, V> (&x)[K], const T* base, int6
 
 constexpr int ROLE = NTHREADS;              // threads that make tiles; as many finish outputs
 
+// What a scan leaves: the outputs; the states (every KT tokens, or a time split's
+// carries); or the states' gradients before a time split's pieces, backwards.
+enum { OUTPUTS, STATES, BACK };
+
 // Two shapes of the forward scan. DEEP: one block per SM, longer tiles and more
 // straight-line code, for grids that give an SM no second block; else two
 // blocks per SM share it.
-template <typename T, int L, int S, int CH, bool OUT, bool DEEP>
+template <typename T, int L, int S, int CH, int MODE, bool DEEP>
 struct FwdShared {
+  static constexpr bool OUT = MODE == OUTPUTS;
   static constexpr int TT = DEEP ? 64 : 32;  // tokens per tile
   static constexpr int GT = DEEP ? 16 : 8;   // tokens of straight-line code in the states' loop
   static constexpr int STATE_THREADS = CH * L, THREADS = STATE_THREADS + (OUT ? 2 : 1) * ROLE;
@@ -247,26 +262,29 @@ struct Ring {
 // warps: the states (L threads of S states per channel, one token after
 // another), the tiles (TT tokens of d, d u, B and C into shared memory, a ring
 // of STAGES) and the outputs (D u, the gate).
-// OUT: the outputs; else states only, for the gradients (ck) or the time split (carry).
+// Backwards (BACK) a tile holds the tokens from the last one on, C for B and the
+// outputs' gradient for d u: g <- a (g + dy C).
 //
 // Why roles: with the same warps for everything the special-function unit waits
 // for loads, softplus and stores (3.70 ms against 0.29 ms for 8192 x 4096 x 16).
 // Why shared memory between them: B and C are one copy for all channels, and a
 // shuffle costs a clock of the same pipe as a load. Counters at 4096 tokens, one
 // sequence: exponentials 57 %, shared-memory wavefronts 54 %, issue 47 %.
-template <typename T, int L, int S, int CH, bool OUT, bool DEEP>
-__global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DEEP || L >= 16 ? 1 : OUT ? 2 : 3)
-    ssm_fwd_kernel(Params p) {
-  using Sh = FwdShared<T, L, S, CH, OUT, DEEP>;
+template <typename T, int L, int S, int CH, int MODE, bool DEEP>
+__global__ void __launch_bounds__(FwdShared<T, L, S, CH, MODE, DEEP>::THREADS,
+                                  DEEP || L >= 16 ? 1 : MODE == OUTPUTS ? 2 : 3) ssm_fwd_kernel(Params p) {
+  using Sh = FwdShared<T, L, S, CH, MODE, DEEP>;
+  constexpr bool OUT = MODE == OUTPUTS;
   constexpr int SN = Sh::STATE_THREADS, TT = Sh::TT, GT = OUT ? Sh::GT : KT;
   extern __shared__ __align__(16) unsigned char smem[];
   Sh& sm = *reinterpret_cast<Sh*>(smem);
   const int role = threadIdx.x < SN ? 0 : 1 + (threadIdx.x - SN) / ROLE;
   const int tid = role == 0 ? threadIdx.x : (threadIdx.x - SN) % ROLE;
-  const int range = blockIdx.y;
+  const int range = blockIdx.y + (MODE == BACK ? 1 : 0);
   const int group = blockIdx.x / p.blocks_per_group, cg = p.C / p.G;
   const int c0 = group * cg + (blockIdx.x % p.blocks_per_group) * CH, c_end = min(c0 + CH, (group + 1) * cg);
-  const bool split_pass = !OUT && p.carry;  // the time split's first pass: the piece that goes on
+  const bool split_pass = MODE == STATES && !p.ck;  // the time split's first pass
+  const int which = MODE == BACK ? CAME_IN : split_pass ? GOES_ON : ALL_PIECES;
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&sm.full[i], ROLE / 32);
@@ -277,7 +295,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
       mbar_init(&sm.y_empty[i], ROLE / 32);
     }
   }
-  if (!split_pass && blockIdx.x == 0 && range == 0)
+  if (MODE != BACK && !split_pass && blockIdx.x == 0 && range == 0)
     for (int s = threadIdx.x; s < p.NS; s += Sh::THREADS) check_packing(p.cu, s, p.T);
   __syncthreads();
   if (role == 0) {  // -------------------------------------------- the states
@@ -299,13 +317,16 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
     for (int i = 0; i < H; ++i) a[i] = make_float2(av[2 * i], av[2 * i + 1]);
     Ring<STAGES> in(0);
     Ring<YSLOTS> yr(1);
-    for_pieces(p, range, split_pass, [&](int seq, int64_t start, int64_t end, int64_t lo, int64_t hi) {
+    for_pieces(p, range, which, [&](int seq, int64_t start, int64_t end, int64_t lo, int64_t hi) {
       const int64_t at = seq * cn + row;
 #pragma unroll
       for (int i = 0; i < 2 * H; ++i) {
         const bool on = i < S && live && q * S + i < p.N;
-        hv[i] = on && p.init && lo == start ? p.init[at + i] : 0.f;
-        if (on && p.run && !split_pass && lo > start) {
+        if (MODE == BACK)
+          hv[i] = on && p.dfin && hi == end ? p.dfin[at + i] : 0.f;
+        else
+          hv[i] = on && p.init && lo == start ? p.init[at + i] : 0.f;
+        if (MODE != BACK && on && p.run && !split_pass && lo > start) {
           // the state before this range: those of the ranges since the sequence's start, decayed
           for (int64_t r = start / p.run; r < range; ++r)
             hv[i] = fmaf(r * p.run <= start ? 0.f : exp2_poly(av[i] * p.sum_d[r * p.C + c0 + ch]), hv[i],
@@ -324,7 +345,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
         const float* cp = &sm.c[OUT ? in.slot : 0][0][q * S];
         unsigned char* yp = &sm.y[yr.slot][0][q][ch % 2 * Sh::ODD + ch / 2 * 16];
         for (int t = 0; t < nt; t += GT, dp += GT * CH, bp += GT * L * S, cp += GT * L * S, yp += GT / 4 * L * Sh::QS) {
-          if (!OUT && p.ck && live) {  // the state before token t, for the gradients
+          if (MODE == STATES && p.ck && live) {  // the state before token t, for the gradients
             const int64_t k = (first_kept(start, seq) + (t0 - start + t) / KT) * cn + row;
 #pragma unroll
             for (int i = 0; i < H; ++i) hv[2 * i] = h[i].x, hv[2 * i + 1] = h[i].y;
@@ -346,7 +367,8 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
             const float2 dd = make_float2(d.x, d.x), du = make_float2(d.y, d.y);
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-              h[i] = __ffma2_rn(pdecay<sizeof(T) == 4>(dd, a[i]), h[i], __fmul2_rn(du, b[i]));
+              const float2 e = pdecay<sizeof(T) == 4>(dd, a[i]);
+              h[i] = MODE == BACK ? __fmul2_rn(e, __ffma2_rn(du, b[i], h[i])) : __ffma2_rn(e, h[i], __fmul2_rn(du, b[i]));
               if (OUT) acc = i ? __ffma2_rn(c[i], h[i], acc) : __fmul2_rn(c[i], h[i]);
             }
             if (OUT) y[j] = S > 1 ? acc.x + acc.y : acc.x;
@@ -365,7 +387,9 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
       }
 #pragma unroll
       for (int i = 0; i < H; ++i) hv[2 * i] = h[i].x, hv[2 * i + 1] = h[i].y;
-      float* to = split_pass ? p.carry + range * cn + row : hi == end && p.fin ? p.fin + at : nullptr;
+      float* to = MODE == BACK ? p.back + range * cn + row
+                  : split_pass ? p.carry + range * cn + row
+                  : hi == end && p.fin ? p.fin + at : nullptr;
       if (live && to) {
 #pragma unroll
         for (int i = 0; i < S; ++i)
@@ -373,7 +397,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
       }
       if (split_pass && live && q == 0) p.sum_d[static_cast<int64_t>(range) * p.C + c0 + ch] = sum;
     });
-    if (p.run && !split_pass && range == 0 && p.fin && live) {  // sequences without tokens
+    if (MODE != BACK && p.run && !split_pass && range == 0 && p.fin && live) {  // sequences without tokens
       for (int s = 0; s < p.NS; ++s) {
         if (bound(p.cu, s + 1, p.T) > bound(p.cu, s, p.T)) continue;
 #pragma unroll
@@ -387,19 +411,22 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
   constexpr int ROWT = CH / 2, TK = ROLE / ROWT, NU = (TT + TK - 1) / TK;
   const int k0 = tid % ROWT * 2, tk = tid / ROWT, valid = max(0, min(2, c_end - c0 - k0));
   if (role == 1) {  // --------------------------------------------- the tiles
-    const T* u = static_cast<const T*>(p.u) + c0 + k0;
+    constexpr bool BACKWARDS = MODE == BACK;
+    const T* u = static_cast<const T*>(BACKWARDS ? p.dout : p.u) + c0 + k0;
     const T* dt = static_cast<const T*>(p.dt) + c0 + k0;
-    const T* bb = static_cast<const T*>(p.b) + group * p.b_sg;
+    const T* z = static_cast<const T*>(p.z) + c0 + k0;
+    const T* bb = BACKWARDS ? static_cast<const T*>(p.c) + group * p.c_sg : static_cast<const T*>(p.b) + group * p.b_sg;
     const T* cc = static_cast<const T*>(p.c) + group * p.c_sg;
+    const int64_t u_st = BACKWARDS ? p.dout_st : p.u_st, b_st = BACKWARDS ? p.c_st : p.b_st;
     float bias[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) bias[i] = p.dt_bias && i < valid ? p.dt_bias[c0 + k0 + i] : 0.f;
     constexpr int NB = (TT * L + ROLE - 1) / ROLE;
-    Vec<T, 2> ru[NU], rd[NU];
+    Vec<T, 2> ru[NU], rd[NU], rz[BACKWARDS ? NU : 1];
     Vec<T, S> rb[NB], rc[NB];
     // rows past the piece's end: its last one again, set to 0 below
     const int n0 = tid % L * S, nv = max(0, min(S, p.N - n0));
-    const bool all = (p.wide & 1) && (p.wide & 2) && (p.wide & 8) && (p.wide & 16) && valid == 2 && nv == S &&
+    const bool all = !BACKWARDS && (p.wide & 1) && (p.wide & 2) && (p.wide & 8) && (p.wide & 16) && valid == 2 && nv == S &&
                      TT % TK == 0 && TT * L % ROLE == 0;
     auto load = [&](int64_t t0, int nt) {
       if (all && nt == TT) {  // nothing to check
@@ -419,25 +446,31 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
         }
         return;
       }
-      auto tok = [&](int k) { return t0 + min(tk + k * TK, nt - 1); };
-      auto bct = [&](int k) { return t0 + min((tid + k * ROLE) / L, nt - 1); };
-      load_rows(ru, u, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
+      // backwards t0 is the tile's last token and the rows go down from it
+      auto tok = [&](int k) { return t0 + (BACKWARDS ? -1 : 1) * min(tk + k * TK, nt - 1); };
+      auto bct = [&](int k) { return t0 + (BACKWARDS ? -1 : 1) * min((tid + k * ROLE) / L, nt - 1); };
+      load_rows(ru, u, u_st, valid, (p.wide & (BACKWARDS ? 32 : 1)) && valid == 2, tok);
       load_rows(rd, dt, p.dt_st, valid, (p.wide & 2) && valid == 2, tok);
-      load_rows(rb, bb + n0, p.b_st, nv, (p.wide & 8) && nv == S, bct);
+      if constexpr (BACKWARDS) {
+        if (p.z) load_rows(rz, z, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
+      }
+      load_rows(rb, bb + n0, b_st, nv, (p.wide & (BACKWARDS ? 16 : 8)) && nv == S, bct);
       if (OUT) load_rows(rc, cc + n0, p.c_st, nv, (p.wide & 16) && nv == S, bct);
     };
     Ring<STAGES> to(1);
-    for_pieces(p, range, split_pass, [&](int, int64_t, int64_t, int64_t lo, int64_t hi) {
-      if (lo < hi) load(lo, static_cast<int>(min(static_cast<int64_t>(TT), hi - lo)));
+    for_pieces(p, range, which, [&](int, int64_t, int64_t, int64_t lo, int64_t hi) {
+      auto first = [&](int64_t t0) { return BACKWARDS ? hi - 1 - (t0 - lo) : t0; };  // a tile's first row
+      if (lo < hi) load(first(lo), static_cast<int>(min(static_cast<int64_t>(TT), hi - lo)));
       for (int64_t t0 = lo; t0 < hi; t0 += TT) {
         const int nt = static_cast<int>(min(static_cast<int64_t>(TT), hi - t0));
         // this tile's; the next one's loads go out before its arithmetic
-        Vec<T, 2> tu[NU], td[NU];
+        Vec<T, 2> tu[NU], td[NU], tz[BACKWARDS ? NU : 1];
         float wb[NB][S], wc[NB][S];
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
           tu[k] = ru[k];
           td[k] = rd[k];
+          if constexpr (BACKWARDS) tz[k] = rz[k];
         }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
@@ -451,14 +484,20 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
             for (int i = 0; i < S; ++i) wb[k][i] = wc[k][i] = 0.f;
           }
         }
-        if (t0 + TT < hi) load(t0 + TT, static_cast<int>(min(static_cast<int64_t>(TT), hi - t0 - TT)));
+        if (t0 + TT < hi) load(first(t0 + TT), static_cast<int>(min(static_cast<int64_t>(TT), hi - t0 - TT)));
         float4 v[NU];
         const bool short_tile = nt < TT || valid < 2;
 #pragma unroll
         for (int k = 0; k < NU; ++k) {
           const float2 r = __fadd2_rn(make_float2(td[k].get(0), td[k].get(1)), make_float2(bias[0], bias[1]));
           const float2 d = pstep<sizeof(T) == 4>(r, p.softplus);
-          const float2 du = __fmul2_rn(d, make_float2(tu[k].get(0), tu[k].get(1)));
+          float2 du = make_float2(tu[k].get(0), tu[k].get(1));
+          if constexpr (BACKWARDS) {
+            const float2 zz = make_float2(tz[k].get(0), tz[k].get(1));
+            if (p.z) du = __fmul2_rn(du, psilu(zz));
+          } else {
+            du = __fmul2_rn(d, du);
+          }
           v[k] = make_float4(d.x, du.x, d.y, du.y);
           if (short_tile) {
             const bool on = tk + k * TK < nt;
@@ -512,7 +551,7 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, OUT, DEEP>::THREADS, DE
       if (p.z) load_rows(rz, z, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
     };
     Ring<YSLOTS> yr(0);
-    for_pieces(p, range, split_pass, [&](int, int64_t, int64_t, int64_t lo, int64_t hi) {
+    for_pieces(p, range, which, [&](int, int64_t, int64_t, int64_t lo, int64_t hi) {
       if (lo < hi) load(lo, static_cast<int>(min(static_cast<int64_t>(TT), hi - lo)));
       for (int64_t t0 = lo; t0 < hi; t0 += TT) {
         const int nt = static_cast<int>(min(static_cast<int64_t>(TT), hi - t0));
@@ -696,18 +735,16 @@ __global__ void __launch_bounds__(NTHREADS) ssm_decode_kernel(DecodeParams p) {
 
 // ---------------------------------------------------------------- backward
 struct BwdParams {
-  Params f;                 // the forward's inputs; ck filled by its states-only pass
-  const void* dout;
-  const float* dfin;        // [NS, C, N] or null: zeros
+  Params f;                 // the forward's inputs, dout and dfin; ck filled by its states-only pass
   void* du;
   void* ddt;
   void* dz;                 // with z
   float* dinit;             // [NS, C, N] or null
-  float* part_a;            // [NS, C, N]
-  float* part_d;            // [2, NS, C]: dD, ddt_bias
+  float* part_a;            // [ranges, C, N]
+  float* part_d;            // [2, ranges, C]: dD, ddt_bias
   float* part_b;            // [channel blocks, T, N]
   float* part_c;
-  int64_t dout_st, du_st, ddt_st, dz_st;
+  int64_t du_st, ddt_st, dz_st;
 };
 
 constexpr int TB = 16;  // tokens per tile of the gradients, in two halves of KT
@@ -745,7 +782,13 @@ struct BwdShared {
 // KT = 8 tokens of decays and states are 64 registers a thread, which leaves 16
 // warps an SM. Counters at 8 x 512 tokens x 4096 x 16: shared-memory wavefronts
 // 66 %, issue 58 %, exponentials 22 %; 839 us at 8 x 1024.
-template <typename T, int L>
+//
+// SPLIT: a range of the time split, its pieces one after another. The states'
+// gradient behind a piece comes from the reverse scans (BACK) of the ranges up to
+// its sequence's end. A form of its own: the unsplit one is short of registers
+// (the same loop with g's start where the split needs it: 44 bytes more spilled,
+// 5 % of the time).
+template <typename T, int L, bool SPLIT>
 __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd_kernel(BwdParams bp) {
   using Sh = BwdShared<L>;
   const Params& p = bp.f;
@@ -755,14 +798,12 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
   Sh& sm = *reinterpret_cast<Sh*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // lane bits of the thread's state group q, its channel and its order f
-  const int b1 = lane >> 1 & 1, hi = lane >> 3, rest = (lane & 1) | (lane >> 2 << 1);
+  const int b1 = lane >> 1 & 1, top = lane >> 3, rest = (lane & 1) | (lane >> 2 << 1);
   const int q = L == 32 ? lane : rest % L;
-  const int chl = warp * (32 / L) + (L == 32 ? 0 : L == 4 ? b1 | hi << 1 : b1 | rest / L << 1);
-  const int f = L == 4 ? hi : L == 8 ? b1 | (lane >> 4) << 1 : L == 16 ? b1 : 0;
-  const int seq = blockIdx.y;
+  const int chl = warp * (32 / L) + (L == 32 ? 0 : L == 4 ? b1 | top << 1 : b1 | rest / L << 1);
+  const int f = L == 4 ? top : L == 8 ? b1 | (lane >> 4) << 1 : L == 16 ? b1 : 0;
   const int group = blockIdx.x / p.blocks_per_group, cg = p.C / p.G;
   const int c0 = group * cg + (blockIdx.x % p.blocks_per_group) * CH, c_end = min(c0 + CH, (group + 1) * cg);
-  const int64_t start = bound(p.cu, seq, p.T), end = max(start, bound(p.cu, seq + 1, p.T));
   const int64_t cn = static_cast<int64_t>(p.C) * p.N;
   const int ch = c0 + chl;
   const bool live = ch < c_end;
@@ -775,7 +816,7 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
       const bool on = live && n < p.N;
       const int64_t at = static_cast<int64_t>(ch) * p.N + n;
       av[i] = on ? p.A[at] * kLog2e : 0.f;
-      gv[i] = on && bp.dfin ? bp.dfin[seq * cn + at] : 0.f;
+      gv[i] = !SPLIT && on && p.dfin ? p.dfin[blockIdx.y * cn + at] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -796,7 +837,25 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
   const int xc = tid % CH, xt = tid / CH * 4;
   const float skip = p.D && c0 + xc < c_end ? p.D[c0 + xc] : 0.f;
   float sum_d = 0.f, sum_bias = 0.f;
-  const int64_t tiles = (end - start + TB - 1) / TB;
+  auto piece = [&](int seq, int64_t start, int64_t end, int64_t lo, int64_t hi) {
+  if constexpr (SPLIT) {  // the states' gradient after the piece
+    // pieces up to the sequence's end: theirs, decayed; the last one brings the final state's
+    int64_t last = blockIdx.y;
+    while (last + 1 < gridDim.y && border((last + 1) * p.run, start) < end) ++last;
+    float gv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = q * 4 + (i ^ f);
+      const bool on = live && n < p.N;
+      const int64_t at = static_cast<int64_t>(ch) * p.N + n;
+      gv[i] = on && p.dfin && hi == end ? p.dfin[seq * cn + at] : 0.f;
+      for (int64_t r = hi < end && on ? last : 0; r > blockIdx.y; --r)
+        gv[i] = fmaf(r == last ? 0.f : exp2_poly(p.A[at] * kLog2e * p.sum_d[r * p.C + ch]), gv[i], p.back[r * cn + at]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) g[i] = make_float2(gv[2 * i], gv[2 * i + 1]);
+  }
+  const int64_t tiles = (hi - start + TB - 1) / TB, tile0 = (lo - start) / TB;
   // A tile's rows as they came and the state kept before its last half: loaded
   // while the tile after it is finished.
   constexpr int NB = (TB * L + NT - 1) / NT;
@@ -817,12 +876,12 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
   const int n0 = tid % L * 4, nv = max(0, min(4, p.N - n0));
   auto load_tile = [&](int64_t tile) {
     const int64_t t0 = start + tile * TB;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(TB), end - t0));
+    const int nt = static_cast<int>(min(static_cast<int64_t>(TB), hi - t0));
     if (m0 < TB) {
       auto tok = [&](int j) { return t0 + min(m0 + j, nt - 1); };
       load_rows(vd, static_cast<const T*>(p.dt) + mc, p.dt_st, valid, (p.wide & 2) && valid == 2, tok);
       load_rows(vu, static_cast<const T*>(p.u) + mc, p.u_st, valid, (p.wide & 1) && valid == 2, tok);
-      load_rows(vo, static_cast<const T*>(bp.dout) + mc, bp.dout_st, valid, (p.wide & 32) && valid == 2, tok);
+      load_rows(vo, static_cast<const T*>(p.dout) + mc, p.dout_st, valid, (p.wide & 32) && valid == 2, tok);
       if (p.z) load_rows(vz, static_cast<const T*>(p.z) + mc, p.z_st, valid, (p.wide & 4) && valid == 2, tok);
     }
     if (tid < TB * L) {
@@ -832,10 +891,10 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
     }
     load_kept(tile, nt > KT ? 1 : 0);
   };
-  if (tiles > 0) load_tile(tiles - 1);
-  for (int64_t k = tiles - 1; k >= 0; --k) {
+  if (tiles > tile0) load_tile(tiles - 1);
+  for (int64_t k = tiles - 1; k >= tile0; --k) {
     const int64_t t0 = start + k * TB;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(TB), end - t0));
+    const int nt = static_cast<int>(min(static_cast<int64_t>(TB), hi - t0));
     // ------------------------------------------------ the tile's operands
     if (m0 < TB) {
 #pragma unroll
@@ -991,7 +1050,7 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
     sm.da[tid] = make_float4(da.x + da_tile[0].x, da.y + da_tile[0].y, da.z + da_tile[1].x, da.w + da_tile[1].y);
     __syncthreads();
     // ------------------------------------------------------- the gradients
-    if (k > 0) load_tile(k - 1);
+    if (k > tile0) load_tile(k - 1);
     for (int i = tid; i < nt * NP; i += NT) {
       const int t = i / NP, n = i % NP;
       if (n >= p.N) continue;
@@ -1039,15 +1098,38 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
     }
     __syncthreads();
   }
+  if (bp.dinit && lo == start) {
+    const float gv[4] = {g[0].x, g[0].y, g[1].x, g[1].y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = q * 4 + (i ^ f);
+      if (live && n < p.N) bp.dinit[seq * cn + static_cast<int64_t>(ch) * p.N + n] = gv[i];
+    }
+  }
+  };
+  if constexpr (SPLIT) {
+    split_pieces(p, blockIdx.y, ALL_PIECES, piece);
+    if (blockIdx.y == 0 && bp.dinit && live) {  // sequences without tokens
+      for (int s = 0; s < p.NS; ++s) {
+        if (bound(p.cu, s + 1, p.T) > bound(p.cu, s, p.T)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = q * 4 + (i ^ f);
+          const int64_t at = s * cn + static_cast<int64_t>(ch) * p.N + n;
+          if (n < p.N) bp.dinit[at] = p.dfin ? p.dfin[at] : 0.f;
+        }
+      }
+    }
+  } else {
+    const int64_t start = bound(p.cu, blockIdx.y, p.T), end = max(start, bound(p.cu, blockIdx.y + 1, p.T));
+    piece(blockIdx.y, start, end, start, end);
+  }
   const float4 da = sm.da[tid];
-  const float dv[4] = {da.x, da.y, da.z, da.w}, gv[4] = {g[0].x, g[0].y, g[1].x, g[1].y};
+  const float dv[4] = {da.x, da.y, da.z, da.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int n = q * 4 + (i ^ f);
-    if (!live || n >= p.N) continue;
-    const int64_t at = seq * cn + static_cast<int64_t>(ch) * p.N + n;
-    bp.part_a[at] = dv[i];
-    if (bp.dinit) bp.dinit[at] = gv[i];
+    if (live && n < p.N) bp.part_a[blockIdx.y * cn + static_cast<int64_t>(ch) * p.N + n] = dv[i];
   }
   // dD and ddt_bias: over the threads of a channel
   float2* sums = reinterpret_cast<float2*>(sm.sum);
@@ -1060,8 +1142,8 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
       v.x += sums[i].x;
       v.y += sums[i].y;
     }
-    bp.part_d[static_cast<int64_t>(seq) * p.C + c0 + tid] = v.x;
-    bp.part_d[(static_cast<int64_t>(p.NS) + seq) * p.C + c0 + tid] = v.y;
+    bp.part_d[static_cast<int64_t>(blockIdx.y) * p.C + c0 + tid] = v.x;
+    bp.part_d[(static_cast<int64_t>(gridDim.y) + blockIdx.y) * p.C + c0 + tid] = v.y;
   }
 }
 
@@ -1080,10 +1162,10 @@ struct ReduceParams {
   void* ddt;
   void* dz;                 // or null
   int64_t T, dB_st, dB_sg, dC_st, dC_sg, du_st, ddt_st, dz_st;
-  int NS, C, N, G, blocks_per_group;
+  int NS, parts, C, N, G, blocks_per_group;  // parts: ranges with sums for dA, dD, ddt_bias
 };
 
-// Sums over the sequences (dA, dD, ddt_bias) and the channel blocks of a group
+// Sums over the ranges (dA, dD, ddt_bias) and the channel blocks of a group
 // (dB, dC), in order; zeros at tokens of no sequence.
 template <typename T>
 __global__ void __launch_bounds__(256) ssm_reduce_kernel(ReduceParams p) {
@@ -1091,7 +1173,7 @@ __global__ void __launch_bounds__(256) ssm_reduce_kernel(ReduceParams p) {
   const int64_t cn = static_cast<int64_t>(p.C) * p.N;
   for (int64_t i = i0; i < cn; i += stride) {
     float a = 0.f;
-    for (int s = 0; s < p.NS; ++s) a += p.part_a[s * cn + i];
+    for (int s = 0; s < p.parts; ++s) a += p.part_a[s * cn + i];
     p.dA[i] = a;
   }
   for (int64_t i = i0; i < 2 * static_cast<int64_t>(p.C); i += stride) {
@@ -1099,7 +1181,7 @@ __global__ void __launch_bounds__(256) ssm_reduce_kernel(ReduceParams p) {
     if (!to) continue;
     const int64_t c = i < p.C ? i : i - p.C;
     float a = 0.f;
-    for (int s = 0; s < p.NS; ++s) a += p.part_d[((i < p.C ? 0 : static_cast<int64_t>(p.NS)) + s) * p.C + c];
+    for (int s = 0; s < p.parts; ++s) a += p.part_d[((i < p.C ? 0 : static_cast<int64_t>(p.parts)) + s) * p.C + c];
     to[c] = a;
   }
   const int64_t lo = bound(p.cu, 0, p.T), hi = bound(p.cu, p.cu ? p.NS : 1, p.T);

@@ -43,18 +43,30 @@ kda_status_t check_ssm(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_
   return KDA_OK;
 }
 
-// The time split of the forward scan: tokens per range, or 0. A range's blocks
-// run beside the other ranges'; a first pass over the pieces that go on in the
-// next range gives each range's start. Where one block per (sequence, channels)
-// leaves half of the SMs idle: as many ranges as fill two blocks per SM, of 256
-// tokens at least (the first pass costs about 3/4 of the second). Measured on
-// 32768 tokens x 1024 channels x 16 states (32 blocks): 444 us in 9 ranges, 1210 us unsplit.
-int64_t scan_run(const SsmArgs& a, int32_t num_seqs, int64_t blocks, int dev) {
+// The time split: tokens per range (a multiple of 32), or 0. A range's blocks run
+// beside the other ranges'; first passes over the pieces that cross a border
+// give each range's start (and, for the gradients, its end). As many ranges as
+// fill two blocks per SM, of `least` tokens at least. The first passes add 0.65 of
+// the forward's work and 0.35 of the gradients', so it is taken where one block per
+// (sequence, channels) leaves SMs idle: at most a quarter of them busy in the
+// forward scan, all of them once for the gradients. And with three times as many
+// ranges as sequences, which may all be alike. Measured, bf16, 16 states:
+//                                 forward, us      gradients, us
+//                                split  unsplit    split  unsplit
+//   32768 x 1024                   442     1113     1444    10604
+//   2048 x 1024                     50       77      155      646
+//   512 x 1024 (gradients only)     27       25       93      182
+//   1000 + 1000, 1024 channels      50       42      146      334
+//   256 of 4 sequences, 2048                         129      109   (9 ranges)
+//   8192 x 2048 (64 blocks)        256      284      752     2702
+//   1024 x 2048                     46       42      144      341
+int64_t split_run(const SsmArgs& a, int32_t num_seqs, int64_t blocks, int64_t most, int64_t least, int dev) {
   const int mode = g_split.load();
   if (mode == 1) return 0;
   if (mode == 2) return a.T >= 128 ? std::max<int64_t>(64, (a.T / 65535 + 32) / 32 * 32) : 0;  // testing
-  if (2 * blocks * num_seqs > g_num_sms[dev] || a.T < 1024) return 0;
-  const int64_t ranges = std::min<int64_t>(2 * g_num_sms[dev] / blocks, a.T / 256);
+  if (blocks * num_seqs > most) return 0;
+  const int64_t ranges = std::min<int64_t>(2 * g_num_sms[dev] / blocks, a.T / least);
+  if (ranges < std::max(4, 3 * num_seqs)) return 0;
   return ((a.T + ranges - 1) / ranges + 31) / 32 * 32;
 }
 
@@ -131,9 +143,9 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.fin = static_cast<float*>(fin);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int sms = g_num_sms[dev];
-  const int64_t run = scan_run(a, num_seqs, scan_blocks(a), dev);
+  const int64_t run = split_run(a, num_seqs, scan_blocks(a), sms / 4, 192, dev);
   if (!run) {
-    const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan(p, true, num_seqs, sms, cs); });
+    const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan(p, sm::OUTPUTS, num_seqs, sms, cs); });
     return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
   }
   if ((st = prepare_pool(dev)) != KDA_OK) return st;
@@ -154,8 +166,8 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.sum_d = reinterpret_cast<float*>(sb + carry_bytes);
   if (in_place) p.fin = reinterpret_cast<float*>(sb + carry_bytes + sum_bytes);
   e = by_type(a.dt, [&](auto m) {
-    const cudaError_t f = ranges > 1 ? m.scan(p, false, ranges - 1, sms, cs) : cudaSuccess;
-    return f == cudaSuccess ? m.scan(p, true, ranges, sms, cs) : f;
+    const cudaError_t f = ranges > 1 ? m.scan(p, sm::STATES, ranges - 1, sms, cs) : cudaSuccess;
+    return f == cudaSuccess ? m.scan(p, sm::OUTPUTS, ranges, sms, cs) : f;
   });
   if (e == cudaSuccess && in_place) e = cudaMemcpyAsync(fin, p.fin, state_bytes, cudaMemcpyDeviceToDevice, cs);
   const cudaError_t ef = cudaFreeAsync(scratch, cs);
@@ -262,11 +274,16 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.f.blocks_per_group = static_cast<int>((a.C / a.G + ch - 1) / ch);
   const int64_t blocks = a.G * p.f.blocks_per_group;
   const size_t cn = static_cast<size_t>(a.C) * a.N;
+  const int sms = g_num_sms[dev];
+  p.f.run = split_run(a, num_seqs, blocks, sms, 64, dev);
+  const int ranges = p.f.run ? static_cast<int>((a.T + p.f.run - 1) / p.f.run) : num_seqs;
   const size_t ck_bytes = round256((static_cast<size_t>(a.T) / sm::KT + num_seqs) * cn * 4);
-  const size_t a_bytes = round256(num_seqs * cn * 4), d_bytes = round256(2 * static_cast<size_t>(num_seqs) * a.C * 4);
+  const size_t a_bytes = round256(ranges * cn * 4), d_bytes = round256(2 * static_cast<size_t>(ranges) * a.C * 4);
+  const size_t carry_bytes = p.f.run ? a_bytes : 0, sum_bytes = p.f.run ? round256(static_cast<size_t>(ranges) * a.C * 4) : 0;
   const size_t b_bytes = round256(static_cast<size_t>(blocks) * a.T * a.N * 4);
   void* scratch = nullptr;
-  cudaError_t e = cudaMallocFromPoolAsync(&scratch, ck_bytes + a_bytes + d_bytes + 2 * b_bytes, g_pool[dev].load(), cs);
+  cudaError_t e = cudaMallocFromPoolAsync(
+      &scratch, ck_bytes + a_bytes + d_bytes + 2 * b_bytes + 2 * carry_bytes + sum_bytes, g_pool[dev].load(), cs);
   if (e != cudaSuccess) return cuda_fail(e);
   unsigned char* sb = static_cast<unsigned char*>(scratch);
   p.f.ck = reinterpret_cast<float*>(sb);
@@ -274,9 +291,15 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.part_d = reinterpret_cast<float*>(sb + ck_bytes + a_bytes);
   p.part_b = reinterpret_cast<float*>(sb + ck_bytes + a_bytes + d_bytes);
   p.part_c = reinterpret_cast<float*>(sb + ck_bytes + a_bytes + d_bytes + b_bytes);
-  p.dout = a.out.data;
-  p.dout_st = a.out.st;
-  p.dfin = static_cast<const float*>(dfin);
+  if (p.f.run) {
+    unsigned char* split = sb + ck_bytes + a_bytes + d_bytes + 2 * b_bytes;
+    p.f.carry = reinterpret_cast<float*>(split);
+    p.f.back = reinterpret_cast<float*>(split + carry_bytes);
+    p.f.sum_d = reinterpret_cast<float*>(split + 2 * carry_bytes);
+  }
+  p.f.dout = a.out.data;
+  p.f.dout_st = a.out.st;
+  p.f.dfin = static_cast<const float*>(dfin);
   p.du = vdu.data;
   p.ddt = vddt.data;
   p.dz = vdz.data;
@@ -308,6 +331,7 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   r.ddt_st = vddt.st;
   r.dz_st = vdz.st;
   r.NS = num_seqs;
+  r.parts = ranges;
   r.C = static_cast<int>(a.C);
   r.N = static_cast<int>(a.N);
   r.G = static_cast<int>(a.G);
@@ -316,8 +340,15 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   const unsigned reduce_blocks =
       static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 8 * static_cast<int64_t>(g_num_sms[dev])));
   e = by_type(a.dt, [&](auto m) {
-    cudaError_t f = m.scan(p.f, false, num_seqs, g_num_sms[dev], cs);
-    if (f == cudaSuccess) f = m.scan_bwd(p, cs);
+    cudaError_t f = cudaSuccess;
+    if (p.f.run && ranges > 1) {
+      sm::Params first = p.f;
+      first.ck = nullptr;
+      f = m.scan(first, sm::STATES, ranges - 1, sms, cs);
+      if (f == cudaSuccess) f = m.scan(first, sm::BACK, ranges - 1, sms, cs);
+    }
+    if (f == cudaSuccess) f = m.scan(p.f, sm::STATES, ranges, sms, cs);
+    if (f == cudaSuccess) f = m.scan_bwd(p, ranges, cs);
     return f == cudaSuccess ? m.scan_reduce(r, reduce_blocks, cs) : f;
   });
   const cudaError_t ef = cudaFreeAsync(scratch, cs);

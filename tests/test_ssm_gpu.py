@@ -179,6 +179,91 @@ def test_scan_time_split_padded_and_bad_boundaries(kda):
         kda.set_time_split(0)
 
 
+def test_gradients_time_split_is_taken_by_itself(kda):
+    """The gradients' time split: within the reference's bounds, the same at each
+    call, and not bitwise the unsplit gradients (so it was taken)."""
+    lens = [900, 3]
+    d = make(lens, 70, 16, 1, torch.float32, seed=44)
+    check_all(kda, d, lens)
+    call = lambda: bwd(kda, d, cu_of(lens), initial_state=d["init"], dfinal_state=d["dfin"])  # noqa: E731
+    a, b = call(), call()
+    try:
+        kda.set_time_split(1)
+        one = call()
+    finally:
+        kda.set_time_split(0)
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    assert not torch.equal(a["dinitial_state"], one["dinitial_state"])
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+def test_gradients_time_split_slow_decays(kda, typ):
+    """Gradients that come through many ranges: decays near one all along, a gradient
+    at the very end and one from the final state only."""
+    lens = [1000]
+    d = make(lens, 40, 8, 1, TYPES[typ], seed=45)
+    d["A"] = d["A"] * 1e-3
+    d["dout"][:990] = 0
+    try:
+        kda.set_time_split(2)
+        check_all(kda, d, lens)
+        d["dout"].zero_()
+        check_all(kda, d, lens)
+    finally:
+        kda.set_time_split(0)
+
+
+def test_gradients_time_split_padded_and_bad_boundaries(kda):
+    T = 200
+    d = make([T], 40, 16, 2, torch.bfloat16, state=False, seed=46)
+    for k in ("u", "dt", "B", "C", "z", "dout"):
+        d[k][153:] = float("nan")
+    try:
+        kda.set_time_split(2)
+        cu = cu_of([100, 0, 53])
+        gr, rg = bwd(kda, d, cu), bwd(kda, d, cu, rows=slice(0, 153))
+        for k in ("du", "ddt", "dz", "dB", "dC"):
+            assert torch.equal(gr[k][:153], rg[k]) and not bool(gr[k][153:].any()), k
+        for k in ("dA", "dD", "ddt_bias", "dinitial_state"):
+            assert torch.equal(gr[k], rg[k]), k
+        assert kda.device_status(reset=True) == 0
+        for bad in ([0, 150, 20, 200], [0, 130, 299, 10 ** 9], [-5, 10, 140, 200], [70, 80, 90, 200]):
+            bwd(kda, d, torch.tensor(bad, dtype=torch.int32, device="cuda"))
+            assert kda.device_status(reset=True) == 1, bad
+    finally:
+        kda.set_time_split(0)
+
+
+def test_gradients_time_split_graphs_and_streams(kda):
+    """Two captured calls that split, replayed side by side and after new inputs, beside an eager one."""
+    lens = [1100]
+    ds = [make(lens, 64, 16, 1, torch.bfloat16, seed=47 + i) for i in range(3)]
+    call = lambda d: bwd(kda, d, initial_state=d["init"], dfinal_state=d["dfin"])  # noqa: E731
+    for d in ds:
+        call(d)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, outs = [], []
+    for d, s in zip(ds, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(call(d))
+        graphs.append(g)
+    for turn in range(2):
+        for d in ds[:2]:
+            d["u"].copy_(torch.randn_like(d["u"]))
+            d["dout"].mul_(0.5)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = call(ds[2])
+        torch.cuda.synchronize()
+        for d, o in zip(ds, outs + [eager]):
+            ref = call(d)
+            assert all(torch.equal(o[k], ref[k]) for k in ref)
+
+
 def test_scan_many_channels(kda):
     lens = [60, 90]
     check_all(kda, make(lens, 1000, 16, 1, torch.bfloat16, seed=6), lens)
