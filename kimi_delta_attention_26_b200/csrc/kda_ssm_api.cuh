@@ -43,7 +43,7 @@ kda_status_t check_ssm(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_
   return KDA_OK;
 }
 
-// The time split: tokens per range (a multiple of 32), or 0. A range's blocks run
+// The time split: tokens per range (a multiple of 16), or 0. A range's blocks run
 // beside the other ranges'; first passes over the pieces that cross a border
 // give each range's start (and, for the gradients, its end). As many ranges as
 // fill two blocks per SM, of `least` tokens at least. The first passes add 0.65 of
@@ -67,7 +67,7 @@ int64_t split_run(const SsmArgs& a, int32_t num_seqs, int64_t blocks, int64_t mo
   if (blocks * num_seqs > most) return 0;
   const int64_t ranges = std::min<int64_t>(2 * g_num_sms[dev] / blocks, a.T / least);
   if (ranges < std::max(4, 3 * num_seqs)) return 0;
-  return ((a.T + ranges - 1) / ranges + 31) / 32 * 32;
+  return ((a.T + ranges - 1) / ranges + 15) / 16 * 16;
 }
 
 int64_t scan_blocks(const SsmArgs& a) {
