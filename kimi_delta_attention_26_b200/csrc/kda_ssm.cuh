@@ -33,6 +33,10 @@ inline int threads_per_channel(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : N <= 
 // Channels of a block of the forward scan and of its gradients.
 inline int scan_channels(int N) { return 128 / threads_per_channel(N); }
 inline int bwd_channels(int N) { return (N <= 32 ? 256 : 128) / threads_per_channel(N); }
+// Blocks that an SM holds: of the scan, by registers; of the gradients, by
+// registers (up to 32 states) and shared memory (above).
+inline int scan_resident(int N) { return N <= 32 ? 2 : 1; }
+inline int bwd_resident(int N) { return N <= 16 || (N > 32 && N <= 64) ? 2 : 1; }
 
 struct Params {
   const void* u;

@@ -45,29 +45,58 @@ kda_status_t check_ssm(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_
 
 // The time split: tokens per range (a multiple of 16), or 0. A range's blocks run
 // beside the other ranges'; first passes over the pieces that cross a border
-// give each range's start (and, for the gradients, its end). As many ranges as
-// fill two blocks per SM, of `least` tokens at least. The first passes add 0.65 of
-// the forward's work and 0.35 of the gradients', so it is taken where one block per
-// (sequence, channels) leaves SMs idle: at most a quarter of them busy in the
-// forward scan, all of them once for the gradients. And with three times as many
-// ranges as sequences, which may all be alike. Measured, bf16, 16 states:
-//                                 forward, us      gradients, us
+// give each range's start (and, for the gradients, its end).
+//
+// Ranges are chosen to fill the places that the device has for blocks once, twice
+// or three times, by the time that a block's chain of tokens takes: rounds x (a
+// range's tokens + a start), times what the first passes add (`alone`), and
+// more where blocks share an SM (`shared`). The split is taken where that is a
+// tenth less than the longest sequence's chain. The lengths are on the device, so
+// several sequences' longest is taken to be 5/4 of the mean.
+// Measured, us (one sequence unless stated; bf16):
+//                                   forward          gradients
 //                                split  unsplit    split  unsplit
-//   32768 x 1024                   442     1113     1444    10604
-//   2048 x 1024                     50       77      155      646
-//   512 x 1024 (gradients only)     27       25       93      182
-//   1000 + 1000, 1024 channels      50       42      146      334
-//   256 of 4 sequences, 2048                         129      109   (9 ranges)
-//   8192 x 2048 (64 blocks)        256      284      752     2702
-//   1024 x 2048                     46       42      144      341
-int64_t split_run(const SsmArgs& a, int32_t num_seqs, int64_t blocks, int64_t most, int64_t least, int dev) {
+//   32768 x 1024 x 16 states       441     1111     1434    10525
+//   8192 x 2048 x 16               229      284      738     2693
+//   2048 x 1024 x 16                48       77      151      640
+//   512 x 1024 x 16                                   76      178
+//   1000 + 1000, 1024 x 16                           140      330
+//   1024 x 4096 x 16                                 228      365
+// and split although the rule leaves it (earlier forms of the rule):
+//   1024 x 2048 x 16                46       42
+//   1000 + 1000, 1024 x 16          50       42
+//   8 of 512 tokens, 256 x 16       34       25
+//   4 of 256 tokens, 2048 x 16                       129      109
+//   8 of 512 tokens, 512 x 24                        294      218
+//   4 of 4096 tokens, 1024 x 24                     2033     1595
+struct SplitCost {
+  int resident;   // blocks that an SM holds
+  int64_t least;  // tokens of a range, at least
+  // in tokens' time of a block that is alone on its SM:
+  int start;      // a block's start
+  int launches;   // the first passes' launches
+  float alone, shared;
+};
+
+int64_t split_run(const SsmArgs& a, int32_t num_seqs, int64_t blocks, const SplitCost& c, int dev) {
   const int mode = g_split.load();
   if (mode == 1) return 0;
   if (mode == 2) return a.T >= 128 ? std::max<int64_t>(64, (a.T / 65535 + 32) / 32 * 32) : 0;  // testing
-  if (blocks * num_seqs > most) return 0;
-  const int64_t ranges = std::min<int64_t>(2 * g_num_sms[dev] / blocks, a.T / least);
-  if (ranges < std::max(4, 3 * num_seqs)) return 0;
-  return ((a.T + ranges - 1) / ranges + 15) / 16 * 16;
+  const int64_t sms = g_num_sms[dev], places = c.resident * sms;
+  if (blocks * num_seqs > sms) return 0;
+  int64_t best = 0;
+  const int64_t longest = num_seqs == 1 ? a.T : a.T * 5 / (4 * static_cast<int64_t>(num_seqs));
+  float best_cost = 0.9f * (longest + c.start);
+  for (int rounds = 1; rounds <= 3; ++rounds) {
+    int64_t ranges = std::min<int64_t>(rounds * places / blocks, a.T / c.least);
+    if (ranges < 2) continue;
+    const int64_t run = ((a.T + ranges - 1) / ranges + 15) / 16 * 16;
+    ranges = (a.T + run - 1) / run;
+    const float cost = ((ranges * blocks + places - 1) / places) * (run + c.start) *
+                           (ranges * blocks > sms && c.resident > 1 ? c.shared : c.alone) + c.launches;
+    if (cost < best_cost) best = run, best_cost = cost;
+  }
+  return best;
 }
 
 int64_t scan_blocks(const SsmArgs& a) {
@@ -143,7 +172,7 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.fin = static_cast<float*>(fin);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int sms = g_num_sms[dev];
-  const int64_t run = split_run(a, num_seqs, scan_blocks(a), sms / 4, 192, dev);
+  const int64_t run = split_run(a, num_seqs, scan_blocks(a), {sm::scan_resident(static_cast<int>(a.N)), 192, 80, 300, 1.65f, 3.f}, dev);
   if (!run) {
     const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan(p, sm::OUTPUTS, num_seqs, sms, cs); });
     return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
@@ -275,7 +304,7 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   const int64_t blocks = a.G * p.f.blocks_per_group;
   const size_t cn = static_cast<size_t>(a.C) * a.N;
   const int sms = g_num_sms[dev];
-  p.f.run = split_run(a, num_seqs, blocks, sms, 64, dev);
+  p.f.run = split_run(a, num_seqs, blocks, {sm::bwd_resident(static_cast<int>(a.N)), 64, 40, 60, 1.35f, 2.16f}, dev);
   const int ranges = p.f.run ? static_cast<int>((a.T + p.f.run - 1) / p.f.run) : num_seqs;
   const size_t ck_bytes = round256((static_cast<size_t>(a.T) / sm::KT + num_seqs) * cn * 4);
   const size_t a_bytes = round256(ranges * cn * 4), d_bytes = round256(2 * static_cast<size_t>(ranges) * a.C * 4);
