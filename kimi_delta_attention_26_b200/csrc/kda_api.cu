@@ -29,7 +29,10 @@ namespace {
 
 thread_local char g_last_cuda_error[256] = "";
 
+// Notes the error and takes it out of the runtime, which would hand it to the
+// next check behind a launch, here or in the caller's own code.
 kda_status_t cuda_fail(cudaError_t e) {
+  cudaGetLastError();
   std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", cudaGetErrorName(e),
                 cudaGetErrorString(e));
   return KDA_ERR_CUDA;
@@ -291,6 +294,16 @@ kda_status_t prepare_pool(int dev) {
   return KDA_OK;
 }
 
+// Scratch from the pool, in stream order. An allocation that does not fit makes
+// the pool grow by what the device has left before it fails, and the pool would
+// keep that for good: it goes back.
+cudaError_t pool_alloc(void** scratch, size_t bytes, int dev, cudaStream_t stream) {
+  const cudaMemPool_t pool = g_pool[dev].load();
+  const cudaError_t e = cudaMallocFromPoolAsync(scratch, bytes, pool, stream);
+  if (e != cudaSuccess) cudaMemPoolTrimTo(pool, 0);
+  return e;
+}
+
 // 0 picks the path that measured faster on B200 for every workload so far:
 // the 16-token one.
 int use_path() {
@@ -526,8 +539,7 @@ kda_status_t launch16_split(const Problem& P, int dev, cudaStream_t stream) {
   kda_status_t st = side_streams(dev, side);
   if (st != KDA_OK) return st;
   void* scratch = nullptr;
-  cudaError_t e = cudaMallocFromPoolAsync(&scratch, 3 * st_bytes + o_bytes + om_bytes + 3 * ring_b,
-                                          g_pool[dev].load(), stream);
+  cudaError_t e = pool_alloc(&scratch, 3 * st_bytes + o_bytes + om_bytes + 3 * ring_b, dev, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   unsigned char* b = static_cast<unsigned char*>(scratch);
   float* sa = reinterpret_cast<float*>(b);
@@ -614,7 +626,7 @@ kda_status_t fwd_pooled(const Problem& P, void* stream) {
   // from the library's pool, released in stream order after the kernel.
   void* ring = nullptr;
   if (P.T > 0) {
-    const cudaError_t e = cudaMallocFromPoolAsync(&ring, ring_bytes(path, P), g_pool[dev].load(), cs);
+    const cudaError_t e = pool_alloc(&ring, ring_bytes(path, P), dev, cs);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   st = launch(P, static_cast<unsigned char*>(ring), path, dev, cs);
@@ -782,7 +794,7 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
   const size_t part_bytes = round256(static_cast<size_t>(b::NPART) * T * H * kda::D * 4);
   const size_t pb_bytes = round256(static_cast<size_t>(b::NPART) * T * H * 4);
   void* scratch = nullptr;
-  cudaError_t e = cudaMallocFromPoolAsync(&scratch, ck_bytes + 3 * part_bytes + pb_bytes, g_pool[dev].load(), cs);
+  cudaError_t e = pool_alloc(&scratch, ck_bytes + 3 * part_bytes + pb_bytes, dev, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   unsigned char* sb = static_cast<unsigned char*>(scratch);
   b::Params p;

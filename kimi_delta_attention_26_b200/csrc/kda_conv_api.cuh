@@ -312,7 +312,7 @@ kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   p.silu = activation == KDA_ACT_SILU;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   void* part = nullptr;
-  cudaError_t e = cudaMallocFromPoolAsync(&part, (p.run_blocks + 1) * (a.W + 1) * a.C * sizeof(float), g_pool[dev].load(), cs);
+  cudaError_t e = pool_alloc(&part, (p.run_blocks + 1) * (a.W + 1) * a.C * sizeof(float), dev, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   p.part = static_cast<float*>(part);
   const dim3 grid(static_cast<unsigned>(p.run_blocks + (num_seqs + cv::NWARPS - 1) / cv::NWARPS), static_cast<unsigned>(cb));

@@ -186,8 +186,7 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   const size_t carry_bytes = round256(static_cast<size_t>(ranges) * a.C * a.N * 4);
   const size_t sum_bytes = round256(static_cast<size_t>(ranges) * a.C * 4);
   void* scratch = nullptr;
-  cudaError_t e =
-      cudaMallocFromPoolAsync(&scratch, carry_bytes + sum_bytes + (in_place ? state_bytes : 0), g_pool[dev].load(), cs);
+  cudaError_t e = pool_alloc(&scratch, carry_bytes + sum_bytes + (in_place ? state_bytes : 0), dev, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   unsigned char* sb = static_cast<unsigned char*>(scratch);
   p.run = run;
@@ -311,8 +310,8 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   const size_t carry_bytes = p.f.run ? a_bytes : 0, sum_bytes = p.f.run ? round256(static_cast<size_t>(ranges) * a.C * 4) : 0;
   const size_t b_bytes = round256(static_cast<size_t>(blocks) * a.T * a.N * 4);
   void* scratch = nullptr;
-  cudaError_t e = cudaMallocFromPoolAsync(
-      &scratch, ck_bytes + a_bytes + d_bytes + 2 * b_bytes + 2 * carry_bytes + sum_bytes, g_pool[dev].load(), cs);
+  cudaError_t e =
+      pool_alloc(&scratch, ck_bytes + a_bytes + d_bytes + 2 * b_bytes + 2 * carry_bytes + sum_bytes, dev, cs);
   if (e != cudaSuccess) return cuda_fail(e);
   unsigned char* sb = static_cast<unsigned char*>(scratch);
   p.f.ck = reinterpret_cast<float*>(sb);

@@ -1,0 +1,51 @@
+"""GPU tests of what the library leaves behind when a call fails, and of its
+status words and first calls."""
+import gc
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import kimi_delta_attention_26_b200 as m
+
+    m.device_status(reset=True)
+    yield m
+    assert m.device_status(reset=True) == 0
+
+
+def too_large(kda):
+    """Gradients whose scratch (over 300 GB) no device holds; the inputs' rows overlap and take no memory."""
+    T, c, n = 1 << 17, 8192, 128
+    rows = torch.zeros(T + c, device="cuda", dtype=torch.bfloat16).as_strided((T, c), (1, 1))
+    bc = torch.zeros(T, 1, n, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(kda.KDAError) as e:
+        kda.kda_ssm_bwd(rows, rows, torch.zeros(c, n, device="cuda"), bc, bc, rows)
+    assert e.value.code == 5 and "out of memory" in str(e.value)
+
+
+def test_a_failed_call_does_not_fail_the_next_one(kda):
+    x, w = torch.randn(60, 72, device="cuda"), torch.randn(72, 4, device="cuda")
+    ref, _ = kda.kda_conv_fwd(x, w)
+    too_large(kda)
+    out, _ = kda.kda_conv_fwd(x, w)
+    assert torch.equal(out, ref)
+    too_large(kda)
+    assert bool(torch.isfinite(torch.exp(-x * x)).all())  # nor a launch of the caller's own
+
+
+def test_a_failed_call_gives_its_memory_back(kda):
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.mem_get_info()[0]
+    too_large(kda)
+    gc.collect()  # the error's traceback holds the binding's own outputs, 4.4 GB
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # a few pages more or less may belong to the driver
+    assert torch.cuda.mem_get_info()[0] >= before - (64 << 20)
