@@ -646,9 +646,11 @@ kda_status_t fwd_pooled(const Problem& P, void* stream) {
 namespace {
 
 // The status words of all translation units, OR-ed and added up, then cleared
-// where asked.
+// where asked. The copies wait for the legacy stream and those it synchronises
+// with, which non-blocking streams are not: hence the device's wait.
 cudaError_t status_words(uint32_t* flags, uint32_t* waits, bool reset_flags, bool reset_waits) {
-  cudaError_t e = cudaMemcpyFromSymbol(flags, kda::g_device_flags, sizeof(uint32_t));
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(flags, kda::g_device_flags, sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(waits, kda::g_wait_timeouts, sizeof(uint32_t));
   const uint32_t zero = 0;
   if (e == cudaSuccess && reset_flags) e = cudaMemcpyToSymbol(kda::g_device_flags, &zero, sizeof(uint32_t));

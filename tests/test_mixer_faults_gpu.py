@@ -49,3 +49,19 @@ def test_a_failed_call_gives_its_memory_back(kda):
     torch.cuda.empty_cache()
     # a few pages more or less may belong to the driver
     assert torch.cuda.mem_get_info()[0] >= before - (64 << 20)
+
+
+def test_the_status_word_waits_for_every_stream(kda):
+    """A call that is still pending on a non-blocking stream (as torch's are) counts."""
+    x, w = torch.randn(60, 72, device="cuda"), torch.randn(72, 4, device="cuda")
+    good, bad = (torch.tensor(b, dtype=torch.int32, device="cuda") for b in ([0, 20, 50, 60], [0, 50, 20, 60]))
+    kda.kda_conv_fwd(x, w, cu_seqlens=good)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for reset in (False, True):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)  # about 50 ms
+            kda.kda_conv_fwd(x, w, cu_seqlens=bad)
+        assert kda.device_status(reset=reset) == 1
+    torch.cuda.synchronize()
+    assert kda.device_status() == 0  # nothing came after the reset
