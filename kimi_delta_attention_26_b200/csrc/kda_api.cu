@@ -645,19 +645,25 @@ kda_status_t fwd_pooled(const Problem& P, void* stream) {
 
 namespace {
 
-// The status words of all translation units, OR-ed and added up, then cleared
-// where asked. The copies wait for the legacy stream and those it synchronises
-// with, which non-blocking streams are not: hence the device's wait.
+// The status words of the translation units that ran, OR-ed and added up, then
+// cleared where asked. The copies wait for the legacy stream and those it
+// synchronises with, which non-blocking streams are not: hence the device's wait.
 cudaError_t status_words(uint32_t* flags, uint32_t* waits, bool reset_flags, bool reset_waits) {
-  cudaError_t e = cudaDeviceSynchronize();
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(flags, kda::g_device_flags, sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaMemcpyFromSymbol(waits, kda::g_wait_timeouts, sizeof(uint32_t));
   const uint32_t zero = 0;
   if (e == cudaSuccess && reset_flags) e = cudaMemcpyToSymbol(kda::g_device_flags, &zero, sizeof(uint32_t));
   if (e == cudaSuccess && reset_waits) e = cudaMemcpyToSymbol(kda::g_wait_timeouts, &zero, sizeof(uint32_t));
-  if (e == cudaSuccess) e = kda::Mixer<__nv_bfloat16>::status(flags, waits, reset_flags, reset_waits);
-  if (e == cudaSuccess) e = kda::Mixer<__half>::status(flags, waits, reset_flags, reset_waits);
-  if (e == cudaSuccess) e = kda::Mixer<float>::status(flags, waits, reset_flags, reset_waits);
+  const uint32_t used = dev < kMaxDevices ? g_mixer_used[dev].load() : 0;
+  auto add = [&](kda_dtype_t dt, auto mixer) {
+    if (e == cudaSuccess && (used >> dt & 1)) e = mixer.status(flags, waits, reset_flags, reset_waits);
+  };
+  add(KDA_BF16, kda::Mixer<__nv_bfloat16>());
+  add(KDA_F16, kda::Mixer<__half>());
+  add(KDA_F32, kda::Mixer<float>());
   return e;
 }
 

@@ -114,9 +114,16 @@ bool aligned(const RowView& v, int64_t bytes) {
 }
 bool aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
+// Bit dt: a kernel of that element type's translation unit may have run on the
+// device, so that its status words count. The others' are 0, and reading them
+// would load that unit's code onto the device (13 ms each).
+std::atomic<uint32_t> g_mixer_used[kMaxDevices];
+
 // f(the launches of the type)
 template <typename F>
-cudaError_t by_type(kda_dtype_t dt, F f) {
+cudaError_t by_type(kda_dtype_t dt, int dev, F f) {
+  const uint32_t bit = 1u << dt;
+  if (!(g_mixer_used[dev].load(std::memory_order_relaxed) & bit)) g_mixer_used[dev].fetch_or(bit);
   if (dt == KDA_BF16) return f(kda::Mixer<__nv_bfloat16>());
   if (dt == KDA_F16) return f(kda::Mixer<__half>());
   return f(kda::Mixer<float>());
@@ -206,7 +213,7 @@ kda_status_t kda_conv_fwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   p.N = num_seqs;
   p.silu = activation == KDA_ACT_SILU;
   const dim3 grid(static_cast<unsigned>(p.run_blocks + (num_seqs + cv::NWARPS - 1) / cv::NWARPS), static_cast<unsigned>(cb));
-  const cudaError_t e = by_type(a.dt, [&](auto m) { return m.conv_fwd(p, a.W, vec, grid, static_cast<cudaStream_t>(stream)); });
+  const cudaError_t e = by_type(a.dt, dev, [&](auto m) { return m.conv_fwd(p, a.W, vec, grid, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
 
@@ -255,7 +262,7 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
   const int per = cv::NTHREADS * (vec ? V : 1);
   const int64_t cb = (a.C + per - 1) / per, rows = std::max<int64_t>(1, int64_t(8) * g_num_sms[dev] / cb);
   const dim3 grid(static_cast<unsigned>(cb), static_cast<unsigned>(std::min({B, rows, int64_t(65535)})));
-  const cudaError_t e = by_type(a.dt, [&](auto m) { return m.conv_decode(p, a.W, vec, grid, static_cast<cudaStream_t>(stream)); });
+  const cudaError_t e = by_type(a.dt, dev, [&](auto m) { return m.conv_decode(p, a.W, vec, grid, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
 
@@ -316,7 +323,7 @@ kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
   if (e != cudaSuccess) return cuda_fail(e);
   p.part = static_cast<float*>(part);
   const dim3 grid(static_cast<unsigned>(p.run_blocks + (num_seqs + cv::NWARPS - 1) / cv::NWARPS), static_cast<unsigned>(cb));
-  e = by_type(a.dt, [&](auto m) { return m.conv_bwd(p, a.W, vec, grid, cs); });
+  e = by_type(a.dt, dev, [&](auto m) { return m.conv_bwd(p, a.W, vec, grid, cs); });
   if (e == cudaSuccess) {
     cv::conv_reduce_kernel<<<dim3(static_cast<unsigned>((a.C + cv::NTHREADS - 1) / cv::NTHREADS), a.W + 1), cv::NTHREADS, 0, cs>>>(
       p.part, p.run_blocks, a.W, a.C, static_cast<float*>(dw), static_cast<float*>(db));

@@ -174,7 +174,7 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   const int sms = g_num_sms[dev];
   const int64_t run = split_run(a, num_seqs, scan_blocks(a), {sm::scan_resident(static_cast<int>(a.N)), 192, 80, 300, 1.65f, 3.f}, dev);
   if (!run) {
-    const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan(p, sm::OUTPUTS, num_seqs, sms, cs); });
+    const cudaError_t e = by_type(a.dt, dev, [&](auto m) { return m.scan(p, sm::OUTPUTS, num_seqs, sms, cs); });
     return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
   }
   if ((st = prepare_pool(dev)) != KDA_OK) return st;
@@ -193,7 +193,7 @@ kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   p.carry = reinterpret_cast<float*>(sb);
   p.sum_d = reinterpret_cast<float*>(sb + carry_bytes);
   if (in_place) p.fin = reinterpret_cast<float*>(sb + carry_bytes + sum_bytes);
-  e = by_type(a.dt, [&](auto m) {
+  e = by_type(a.dt, dev, [&](auto m) {
     const cudaError_t f = ranges > 1 ? m.scan(p, sm::STATES, ranges - 1, sms, cs) : cudaSuccess;
     return f == cudaSuccess ? m.scan(p, sm::OUTPUTS, ranges, sms, cs) : f;
   });
@@ -254,7 +254,7 @@ kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const
   const int quad = 4 * io_bytes(a.dt);
   p.wide = (a.N % 4 == 0 && aligned(a.b, quad) ? 1 : 0) | (a.N % 4 == 0 && aligned(a.c, quad) ? 2 : 0) |
            (a.N % 4 == 0 && aligned(sp, 16) && aligned(a.A, 16) ? 4 : 0) | (a.G > 1 && a.C / a.G % 4 != 0 ? 8 : 0);
-  const cudaError_t e = by_type(a.dt, [&](auto m) { return m.scan_decode(p, B_, static_cast<cudaStream_t>(stream)); });
+  const cudaError_t e = by_type(a.dt, dev, [&](auto m) { return m.scan_decode(p, B_, static_cast<cudaStream_t>(stream)); });
   return e != cudaSuccess ? cuda_fail(e) : KDA_OK;
 }
 
@@ -367,7 +367,7 @@ kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kd
   const int64_t most = std::max<int64_t>(a.T * a.G * a.N, static_cast<int64_t>(cn));
   const unsigned reduce_blocks =
       static_cast<unsigned>(std::min<int64_t>((most + 255) / 256, 8 * static_cast<int64_t>(g_num_sms[dev])));
-  e = by_type(a.dt, [&](auto m) {
+  e = by_type(a.dt, dev, [&](auto m) {
     cudaError_t f = cudaSuccess;
     if (p.f.run && ranges > 1) {
       sm::Params first = p.f;

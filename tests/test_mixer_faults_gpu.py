@@ -65,3 +65,41 @@ def test_the_status_word_waits_for_every_stream(kda):
         assert kda.device_status(reset=reset) == 1
     torch.cuda.synchronize()
     assert kda.device_status() == 0  # nothing came after the reset
+
+
+STATUS_TIMES = """
+import time, torch
+import kimi_delta_attention_26_b200 as kda
+q = torch.zeros(16, 1, 128, dtype=torch.bfloat16, device="cuda")
+g = torch.zeros(16, 1, 128, device="cuda")
+kda.kda_fwd(q, q, q, g, g[..., 0].contiguous())
+def each():
+    kda.device_status()
+    t = []
+    for _ in range(50):
+        t0 = time.perf_counter()
+        kda.device_status()
+        t.append(time.perf_counter() - t0)
+    return sorted(t)[25]
+t0 = time.perf_counter()
+kda.device_status()
+first, before = time.perf_counter() - t0, each()
+for t in (torch.bfloat16, torch.float16, torch.float32):
+    kda.kda_conv_fwd(torch.zeros(4, 8, dtype=t, device="cuda"), torch.zeros(8, 4, device="cuda"))
+print(first, before, each())
+"""
+
+
+def test_the_status_word_reads_only_what_ran(kda):
+    """Reading the status after KDA calls alone copies two words, not eight
+    (2 copies and 2 resets against 8 and 2), and loads no other code onto the device."""
+    import subprocess
+    import sys
+
+    from tests.conftest import ROOT
+
+    out = subprocess.run([sys.executable, "-c", STATUS_TIMES], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr
+    first, before, after = (float(v) for v in out.stdout.split()[-3:])
+    assert before < 0.7 * after, (first, before, after)
+    assert first < 0.010, (first, before, after)  # three units' code took 40 ms
