@@ -270,7 +270,9 @@ kda_status_t check_device(int dev) {
   return KDA_OK;
 }
 
-// The pool of kda_fwd's scratch rings, created once per device.
+// The pool of the calls' scratch, created once per device. Creating it is no work
+// of a stream, but a capture in this thread or another refuses it as it does any
+// allocation: allowed for the time of it, so that a first call can be captured.
 kda_status_t prepare_pool(int dev) {
   if (g_pool[dev].load(std::memory_order_acquire)) return KDA_OK;
   std::lock_guard<std::mutex> lock(g_setup_mutex);
@@ -282,14 +284,15 @@ kda_status_t prepare_pool(int dev) {
   props.location.type = cudaMemLocationTypeDevice;
   props.location.id = dev;
   cudaMemPool_t pool = nullptr;
-  cudaError_t e = cudaMemPoolCreate(&pool, &props);
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
   if (e != cudaSuccess) return cuda_fail(e);
+  e = cudaMemPoolCreate(&pool, &props);
   uint64_t keep = ~0ull;
-  e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-  if (e != cudaSuccess) {
+  if (e == cudaSuccess && (e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess)
     cudaMemPoolDestroy(pool);
-    return cuda_fail(e);
-  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) return cuda_fail(e);
   g_pool[dev].store(pool, std::memory_order_release);
   return KDA_OK;
 }

@@ -103,3 +103,51 @@ def test_the_status_word_reads_only_what_ran(kda):
     first, before, after = (float(v) for v in out.stdout.split()[-3:])
     assert before < 0.7 * after, (first, before, after)
     assert first < 0.010, (first, before, after)  # three units' code took 40 ms
+
+
+FIRST_CALL = """
+import sys, torch
+import kimi_delta_attention_26_b200 as kda
+g = torch.Generator(device="cuda").manual_seed(1)
+rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+T, c = 1100, 64
+x, w, A = rnd(T, c), rnd(c, 4), -torch.exp(rnd(c, 16))
+B, C, dt = rnd(T, 1, 16), rnd(T, 1, 16), rnd(T, c)
+k = torch.nn.functional.normalize(rnd(T, 1, 128), dim=-1).bfloat16()
+f = (k, k, k, -torch.rand(T, 1, 128, device="cuda"), torch.rand(T, 1, device="cuda"))
+calls = {
+    "conv_bwd": lambda: kda.kda_conv_bwd(x, w, x).values(),
+    "ssm_fwd": lambda: kda.kda_ssm_fwd(x, dt, A, B, C),
+    "ssm_bwd": lambda: kda.kda_ssm_bwd(x, dt, A, B, C, x).values(),
+    "fwd": lambda: kda.kda_fwd(*f),
+    "bwd": lambda: kda.kda_bwd(*f, k).values(),
+}
+call = calls[sys.argv[1]]
+kda.set_time_split(int(sys.argv[2]))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = [t for t in call() if t is not None]
+for t in out:
+    t.zero_()
+for _ in range(2):
+    graph.replay()
+torch.cuda.synchronize()
+assert all(torch.isfinite(t).all() for t in out)
+assert all(torch.equal(a, b) for a, b in zip(out, [t for t in call() if t is not None]))
+assert kda.device_status() == 0
+"""
+
+
+@pytest.mark.parametrize("name,split", [("conv_bwd", 0), ("ssm_fwd", 2), ("ssm_bwd", 1), ("ssm_bwd", 2), ("fwd", 1),
+                                        ("fwd", 2), ("bwd", 0)])
+def test_a_first_call_can_be_captured(kda, name, split):
+    """The first call of a process that takes scratch, in a capture."""
+    import subprocess
+    import sys
+
+    from tests.conftest import ROOT
+
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL, name, str(split)], cwd=ROOT, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0, out.stderr
