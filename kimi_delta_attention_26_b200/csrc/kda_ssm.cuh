@@ -143,6 +143,13 @@ __device__ __forceinline__ float exp2_poly(float x) {
   return x == x ? y : x;
 }
 
+// h 2^x, the decay of a whole range of tokens, in two halves: with rates above 0
+// 2^x alone can overflow where the product does not, and nothing stays nothing.
+__device__ __forceinline__ float decayed(float h, float x) {
+  const float e = exp2_poly(0.5f * x);
+  return h == 0.f ? 0.f : h * e * e;
+}
+
 // The decay 2^(d a) of a token for two states. ex2.approx is low by 2e-8 on
 // average (measured, 5e-9 to 3e-8 for exponents between -1 and 0), which a state
 // that lasts n tokens takes n times; 1.5e-8 on the exponent, which the
@@ -333,8 +340,8 @@ __global__ void __launch_bounds__(FwdShared<T, L, S, CH, MODE, DEEP>::THREADS,
         if (MODE != BACK && on && p.run && !split_pass && lo > start) {
           // the state before this range: those of the ranges since the sequence's start, decayed
           for (int64_t r = start / p.run; r < range; ++r)
-            hv[i] = fmaf(r * p.run <= start ? 0.f : exp2_poly(av[i] * p.sum_d[r * p.C + c0 + ch]), hv[i],
-                         p.carry[r * cn + row + i]);
+            hv[i] = (r * p.run <= start ? 0.f : decayed(hv[i], av[i] * p.sum_d[r * p.C + c0 + ch])) +
+                    p.carry[r * cn + row + i];
         }
       }
 #pragma unroll
@@ -854,7 +861,7 @@ __global__ void __launch_bounds__(BwdShared<L>::THREADS, L == 4 ? 2 : 1) ssm_bwd
       const int64_t at = static_cast<int64_t>(ch) * p.N + n;
       gv[i] = on && p.dfin && hi == end ? p.dfin[seq * cn + at] : 0.f;
       for (int64_t r = hi < end && on ? last : 0; r > blockIdx.y; --r)
-        gv[i] = fmaf(r == last ? 0.f : exp2_poly(p.A[at] * kLog2e * p.sum_d[r * p.C + ch]), gv[i], p.back[r * cn + at]);
+        gv[i] = (r == last ? 0.f : decayed(gv[i], p.A[at] * kLog2e * p.sum_d[r * p.C + ch])) + p.back[r * cn + at];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) g[i] = make_float2(gv[2 * i], gv[2 * i + 1]);

@@ -213,6 +213,24 @@ def test_gradients_time_split_slow_decays(kda, typ):
         kda.set_time_split(0)
 
 
+@pytest.mark.parametrize("typ", ["bf16", "f32"])
+def test_time_split_growing_states(kda, typ):
+    """Rates above 0: a range's growth (e^64 to e^140) overflows fp32, but the tokens
+    with inputs are the last 30 and those with output gradients the first 30, so no
+    state and no gradient does. A product's exponents add up to at most 30 * 2.2 = 66,
+    each with a relative 2^-23 (33 of the tolerance's steps, of which there are 640)."""
+    d = make([640], 40, 8, 1, TYPES[typ], softplus=False, state=False, seed=48)
+    g = torch.Generator().manual_seed(49)
+    d["A"] = (0.5 + 0.5 * torch.rand(40, 8, generator=g)).cuda()
+    d["dt"] = (2 + 0.2 * torch.rand(640, 40, generator=g)).to(TYPES[typ]).cuda()
+    d["u"][:610], d["dout"][30:] = 0, 0
+    try:
+        kda.set_time_split(2)
+        check_all(kda, d, [640])
+    finally:
+        kda.set_time_split(0)
+
+
 def test_gradients_time_split_padded_and_bad_boundaries(kda):
     T = 200
     d = make([T], 40, 16, 2, torch.bfloat16, state=False, seed=46)
