@@ -128,6 +128,55 @@ def test_conv_decode_slots(kda):
     assert kda.kda_conv_decode(d["x"][:0], d["weight"], pool, d["bias"]).shape == (0, 40)
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("C", [12288, 12289])
+def test_conv_decode_many_requests(kda, C, typ, in_place):
+    """More requests than blocks: a block takes several, and loads the next one's
+    state and token before it writes this one's. The bits of one call per request.
+    Bad slots between good ones are skipped."""
+    B, P, W = 131, 140, 4
+    g = torch.Generator().manual_seed(C)
+    d = make([B], C, W, TYPES[typ], state=False, seed=C)
+    pool = torch.randn(P, W - 1, C, generator=g).to(TYPES[typ]).cuda()
+    slots = torch.randperm(P, generator=g)[:B]
+    bad = {0: -1, 30: P, 49: 2 ** 31 - 1, 98: -2 ** 31, 130: P + 5}
+    for b, s in bad.items():
+        slots[b] = s
+    idx = slots.int().cuda()
+    ref_pool, ref = pool.clone(), torch.full_like(d["x"], 7.0)
+    for b in range(B):
+        if b not in bad:
+            s = int(slots[b])
+            kda.kda_conv_decode(d["x"][b:b + 1], d["weight"], ref_pool[s:s + 1], d["bias"], out=ref[b:b + 1])
+    x = d["x"].clone()
+    out = x if in_place else torch.full_like(x, 7.0)
+    kda.kda_conv_decode(x, d["weight"], pool, d["bias"], state_indices=idx, out=out)
+    assert kda.device_status(reset=True) == 4
+    good = [b for b in range(B) if b not in bad]
+    assert torch.equal(out[good], ref[good]) and torch.equal(pool, ref_pool)
+    assert torch.equal(out[list(bad)], d["x"][list(bad)] if in_place else ref[list(bad)])
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("C", [1000, 333])
+def test_conv_alone_as_packed(kda, C, typ):
+    """A sequence gives the same bits alone and in a batch."""
+    lens = [130, 0, 47, 2, 400]
+    d = make(lens, C, 4, TYPES[typ], seed=16)
+    cu = cu_of(lens)
+    out, fin = kda.kda_conv_fwd(d["x"], d["weight"], d["bias"], "silu", cu, d["init"])
+    gr = kda.kda_conv_bwd(d["x"], d["weight"], d["dout"], d["bias"], "silu", cu, d["init"], d["dfin"])
+    for k, (a, b) in enumerate(R.spans(lens)):
+        one = slice(k, k + 1)
+        o, f = kda.kda_conv_fwd(d["x"][a:b], d["weight"], d["bias"], "silu", None, d["init"][one])
+        g = kda.kda_conv_bwd(d["x"][a:b], d["weight"], d["dout"][a:b], d["bias"], "silu", None, d["init"][one],
+                             d["dfin"][one])
+        assert torch.equal(o, out[a:b]) and torch.equal(f, fin[one]), k
+        assert torch.equal(g["dx"], gr["dx"][a:b]), k
+        assert torch.equal(g["dinitial_state"], gr["dinitial_state"][one]), k
+
+
 def test_conv_padded_batch(kda):
     """Tokens behind the last sequence: outputs left as they were (whatever the
     inputs hold there), gradients zero."""
