@@ -287,6 +287,52 @@ def test_scan_many_channels(kda):
     check_all(kda, make(lens, 1000, 16, 1, torch.bfloat16, seed=6), lens)
 
 
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("n", [4, 8, 16, 24])
+def test_scan_many_blocks(kda, n, typ):
+    """More blocks than SMs (the form with two blocks on an SM): several full tiles
+    of every sequence, with the paired and wide loads of even, aligned rows."""
+    lens = [100 + 7 * i % 40 for i in range(15)] + [0]
+    d = make(lens, 384, n, 1, TYPES[typ], seed=70 + n)
+    try:
+        kda.set_time_split(1)
+        check_all(kda, d, lens)
+    finally:
+        kda.set_time_split(0)
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("n,c", [(40, 40), (64, 40), (128, 20), (128, 640)])
+def test_scan_many_states_aligned(kda, n, c, typ):
+    """More than 32 states with even, aligned rows: full tiles in paired and wide loads."""
+    lens = [140, 33, 64]
+    check_all(kda, make(lens, c, n, 1, TYPES[typ], seed=n + c), lens)
+
+
+@pytest.mark.parametrize("typ", list(TYPES))
+@pytest.mark.parametrize("n", [8, 16, 24, 64])
+def test_scan_alone_as_packed(kda, n, typ):
+    """Unsplit, a sequence gives the same bits alone and in a batch, whose blocks
+    outnumber the SMs where its own do not."""
+    lens = [130, 0, 47, 200] + [1] * 12
+    d = make(lens, 384, n, 1, TYPES[typ], seed=80 + n)
+    try:
+        kda.set_time_split(1)
+        cu = cu_of(lens)
+        out, fin = fwd(kda, d, cu, initial_state=d["init"])
+        gr = bwd(kda, d, cu, initial_state=d["init"], dfinal_state=d["dfin"])
+        for k, (a, b) in enumerate(R.spans(lens)[:5]):
+            r, one = slice(a, b), slice(k, k + 1)
+            o, f = fwd(kda, d, rows=r, initial_state=d["init"][one])
+            g = bwd(kda, d, rows=r, initial_state=d["init"][one], dfinal_state=d["dfin"][one])
+            assert torch.equal(o, out[r]) and torch.equal(f, fin[one]), k
+            for name in ("du", "ddt", "dz", "dB", "dC"):
+                assert torch.equal(g[name], gr[name][r]), (k, name)
+            assert torch.equal(g["dinitial_state"], gr["dinitial_state"][one]), k
+    finally:
+        kda.set_time_split(0)
+
+
 def test_scan_extreme_steps(kda):
     """Steps so large that the state is forgotten at once, and so small that it
     stays; softplus far above and below its bend."""
