@@ -27,7 +27,9 @@
  *   - The caller owns all inputs and outputs. kda_fwd takes a scratch ring
  *     (num_seqs * H slots of KDA_RING_BYTES_PER_PAIR bytes) from a
  *     library-private stream-ordered memory pool and returns it in stream
- *     order after the kernel; the pool keeps its memory for later calls.
+ *     order after the kernel; the pool keeps its memory for later calls. A call
+ *     whose scratch does not fit returns KDA_ERR_CUDA and gives the pool's unused
+ *     memory back to the device.
  *   - Work is enqueued on `stream` (a cudaStream_t; NULL = legacy default
  *     stream) and the call returns without synchronising.
  *   - Argument errors are reported synchronously through the return code and
@@ -37,7 +39,7 @@
  *     a sequence gives bit-identical results alone or inside any batch.
  *   - First-call setup per device (capability check, kernel attributes, the
  *     memory pool) is guarded by a lock: concurrent first calls from several
- *     host threads are safe.
+ *     host threads are safe, and a first call may be captured into a CUDA graph.
  */
 #ifndef KDA_H_
 #define KDA_H_
@@ -352,17 +354,23 @@ kda_status_t kda_bwd(const kda_tensor_t* q, const kda_tensor_t* k, const kda_ten
  *   - Token tensors are bf16, fp16 or fp32 (all of a call the same), parameters
  *     fp32, sums fp32, each result rounded once. Token tensors may have any
  *     positive token (and group) strides and need only their element's
- *     alignment; the last dimension must have stride 1. Rows of 16-byte
- *     alignment and stride are read 16 bytes at a time. The other tensors are
- *     contiguous.
+ *     alignment; the last dimension must have stride 1. The other tensors are
+ *     contiguous. Wide accesses, which are faster, are made where they can be: by the
+ *     convolution 8 bytes where x, out (dout, dx) and the states have 8-byte
+ *     alignment and strides and C is a multiple of 8 bytes of elements; by the scan
+ *     two channels where C / G is even (or G = 1) and a row's address and stride are
+ *     a multiple of them, and four states where S is a multiple of 4 and the same
+ *     holds for B and C (single tokens: and A and the states are 16-byte aligned).
  *   - cu_seqlens as for kda_fwd, except that cu[N] may be less than T (a padded
  *     batch): the tokens behind the last sequence are not read, their outputs
  *     are left as they were and their gradients are zero. Zero-length sequences
  *     and T = 0 are allowed. Violations are recorded in the device status word.
  *   - An output may not overlap an input or another output (KDA_ERR_OVERLAP)
  *     unless the call says so.
- *   - Results are deterministic: no atomics on data. kda_conv_bwd, kda_ssm_bwd
- *     and a time-split kda_ssm_fwd take scratch from the library's pool.
+ *   - Results are deterministic: no atomics on data. Alone and in a batch a
+ *     sequence gives the same outputs, states and token gradients, bitwise, as long
+ *     as the scan is not split in time. kda_conv_bwd, kda_ssm_bwd and a time-split
+ *     kda_ssm_fwd take scratch from the library's pool.
  *   - Calls can be captured into CUDA graphs and run on any stream.
  */
 #define KDA_ACT_NONE 0
@@ -397,6 +405,7 @@ kda_status_t kda_conv_decode(const kda_tensor_t* x, const kda_tensor_t* weight, 
  *   dx              [T, C] of x's type, written in full
  *   dweight         fp32 [C, W]; dbias fp32 [C] or NULL (not written)
  *   dinitial_state  [N, W - 1, C] of x's type, or NULL (not written)
+ * Scratch: 4 C (W + 1) bytes for every 64 to 1024 tokens.
  */
 kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, const kda_tensor_t* bias,
                           int32_t activation, const int32_t* cu_seqlens, int32_t num_seqs,
@@ -425,7 +434,10 @@ kda_status_t kda_conv_bwd(const kda_tensor_t* x, const kda_tensor_t* weight, con
  * Where there are few channels and sequences for the device's SMs, ranges of the
  * packed tokens are scanned side by side (the time split; kda_set_time_split
  * applies: 0 automatic, 1 never, 2 from 128 tokens on, for testing). Results
- * then agree with the unsplit scan within rounding, not bitwise.
+ * then agree with the unsplit scan within rounding, not bitwise. Scratch then: 4 C S
+ * bytes a range, and the final states' bytes where they replace the initial ones.
+ * The choice goes by num_seqs, not by the lengths, which are on the device: one
+ * long sequence packed with many short ones may stay unsplit.
  */
 kda_status_t kda_ssm_fwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
                          const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,
@@ -451,9 +463,15 @@ kda_status_t kda_ssm_decode(const kda_tensor_t* u, const kda_tensor_t* dt, const
  *   dB, dC          [T, G, S] of u's type (sums over a group's channels)
  *   dA              fp32 [C, S]; dD, ddt_bias fp32 [C] or NULL (not written)
  *   dinitial_state  fp32 [N, C, S] or NULL (not written)
- * All written in full. Scratch from the pool: a state every 8 tokens (C S / 2
- * bytes a token) and the partial sums of dB and dC. The time split applies as
- * for kda_ssm_fwd, from more channels and fewer tokens on.
+ * All written in full. The time split applies as for kda_ssm_fwd, from more
+ * channels and fewer tokens on.
+ * Scratch from the pool: a state every 8 tokens, the blocks' sums of dB and dC
+ * (64 channels a block up to 16 states, then 32, 8 and 4) and those of dA:
+ *     states S            1..16     17..32    33..64    65..128
+ *     bytes a token       5/8 C S   3/4 C S   3/2 C S   5/2 C S
+ *   (channels of a group rounded up to a block's), and 8 C S bytes a sequence, or
+ *   4 C S a sequence and 12 C S a range where it is split. 8192 tokens of 4096
+ *   channels: 335 MB with 16 states, 10.7 GB with 128. The pool keeps it.
  */
 kda_status_t kda_ssm_bwd(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_tensor_t* A, const kda_tensor_t* B,
                          const kda_tensor_t* C, const kda_tensor_t* D, const kda_tensor_t* z,
@@ -482,7 +500,7 @@ const char* kda_last_cuda_error(void);
  *   KDA_DEVICE_BAD_STATE_INDEX kda_decode, kda_conv_decode or kda_ssm_decode met
  *                              a state index outside [0, P)
  *                              (that request was skipped)
- * Writes the bits to *flags (synchronising with the device), clears them when
+ * Writes the bits to *flags (synchronising with the device, every stream of it), clears them when
  * `reset` is non-zero, and returns KDA_ERR_DEVICE if any bit is set, else
  * KDA_OK (or KDA_ERR_NULL / KDA_ERR_CUDA).
  */

@@ -158,8 +158,8 @@ def set_schedule(mode: int, clusters: int = 0) -> None:
 
 def device_status(reset: bool = True) -> int:
     """The device status word (bit 0: a bad cu_seqlens was seen, bit 1: a
-    bounded in-kernel wait ran out, bit 2: kda_decode met a state index out of
-    range); synchronises with the device."""
+    bounded in-kernel wait ran out, bit 2: a decode call met a state index out
+    of range); synchronises with the device."""
     n = ctypes.c_uint32(0)
     rc = _lib.kda_device_status(ctypes.byref(n), 1 if reset else 0)
     if rc not in (0, 9):

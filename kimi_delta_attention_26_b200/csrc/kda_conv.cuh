@@ -11,15 +11,17 @@
 // positions before the first token).
 //
 // Each input is read once and each output written once: bound by HBM. A warp
-// takes 32 x V channels (V = 8 bytes of them, 16 for single tokens, where
-// strides and addresses allow, else 1) of a run of tokens, carries the last
-// inputs in registers and loads four tokens while it computes four.
+// takes 32 x V channels (V = 8 bytes of them where strides and addresses allow,
+// else 1) of a run of tokens, carries the last inputs in registers and loads four
+// tokens while it computes four.
 // All arithmetic is fp32; the outputs are rounded once.
 //
-// Measured (bf16, 4 taps, SiLU): 18264 tokens x 12288 channels 174 us (5.2 TB/s,
-// 79 % of the copy rate; 16-byte accesses, 183 to 231 registers: 284 us), the
+// Measured (bf16, 4 taps, SiLU): 18264 tokens x 12288 channels 175 us (5.1 TB/s,
+// 78 % of the copy rate; 16-byte accesses, 183 to 231 registers: 284 us), the
 // gradients of 8192 tokens 150 + 5 us (4.0 TB/s; two channels a thread: 190 us),
-// one token of 256 requests 10 us (5.0 TB/s).
+// one token of 256 requests 10 us (4.9 TB/s). fp32: 8192 tokens 143 us (5.6
+// TB/s; bf16 88), their gradients 241, one token of 256 requests 14.2 us (7.1 TB/s,
+// part of it from L2).
 #pragma once
 
 #include <type_traits>

@@ -10,7 +10,7 @@ namespace kda {
 
 template <typename T>
 struct Mixer {
-  // `vec`: accesses of conv::RUN_BYTES (single tokens: 16 bytes) are possible
+  // `vec`: accesses of conv::RUN_BYTES are possible
   static cudaError_t conv_fwd(const conv::Params& p, int W, bool vec, dim3 grid, cudaStream_t stream);
   static cudaError_t conv_decode(const conv::DecodeParams& p, int W, bool vec, dim3 grid, cudaStream_t stream);
   static cudaError_t conv_bwd(const conv::BwdParams& p, int W, bool vec, dim3 grid, cudaStream_t stream);

@@ -68,8 +68,8 @@ cudaError_t Mixer<T>::conv_bwd(const conv::BwdParams& p, int W, bool vec, dim3 g
 
 // With no more blocks than SMs the deeper shape (where its shared memory fits
 // and states come in fours), else two blocks per SM. Measured (8192 tokens x 4096
-// channels x 16 states, bf16): one sequence, 128 blocks, 309 us deep and 347 us
-// not; 8 sequences, 1024 blocks, 288 us and 247 us.
+// channels x 16 states, bf16): one sequence, 128 blocks, 286 us deep and 331 us
+// not; 8 sequences, 1024 blocks, 264 us and 236 us.
 template <typename T>
 cudaError_t Mixer<T>::scan(ssm::Params p, int mode, int ranges, int sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;

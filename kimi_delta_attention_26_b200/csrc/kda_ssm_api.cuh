@@ -53,22 +53,26 @@ kda_status_t check_ssm(const kda_tensor_t* u, const kda_tensor_t* dt, const kda_
 // more where blocks share an SM (`shared`). The split is taken where that is a
 // tenth less than the longest sequence's chain. The lengths are on the device, so
 // several sequences' longest is taken to be 5/4 of the mean.
-// Measured, us (one sequence unless stated; bf16):
+// Measured, us (one sequence unless stated; bf16), the split as the rule takes it:
 //                                   forward          gradients
 //                                split  unsplit    split  unsplit
-//   32768 x 1024 x 16 states       441     1111     1434    10525
-//   8192 x 2048 x 16               229      284      738     2693
-//   2048 x 1024 x 16                48       77      151      640
-//   512 x 1024 x 16                                   76      178
-//   1000 + 1000, 1024 x 16                           140      330
-//   1024 x 4096 x 16                                 228      365
-// and split although the rule leaves it (earlier forms of the rule):
-//   1024 x 2048 x 16                46       42
-//   1000 + 1000, 1024 x 16          50       42
-//   8 of 512 tokens, 256 x 16       34       25
-//   4 of 256 tokens, 2048 x 16                       129      109
-//   8 of 512 tokens, 512 x 24                        294      218
-//   4 of 4096 tokens, 1024 x 24                     2033     1595
+//   32768 x 1024 x 16 states       444     1112     1435    10512
+//   8192 x 2048 x 16               231      286      742     2685
+//   2048 x 1024 x 16                49       78      157      648
+//   512 x 1024 x 16                                   81      185
+//   1000 + 1000, 1024 x 16                           144      334
+//   1024 x 4096 x 16                                 232      367
+// and by force where the rule leaves it:
+//   1024 x 2048 x 16                48       43
+//   1000 + 1000, 1024 x 16          45       43
+//   8 of 512 tokens, 256 x 16       41       26
+//   4 of 256 tokens, 2048 x 16                       133      114
+//   8 of 512 tokens, 512 x 24                        275      224
+//   4 of 4096 tokens, 1024 x 24                     2013     1593
+// Where it is wrong, one long sequence among short ones:
+//   32000 + 7 of 110, 1024 x 16    448     1259     1458    10377  (the gradients do split)
+//   32000 + 15 of 50, 1024 x 16                     1477    10283
+//   8192 + 1 + 1, 4096 x 16        421      533     1382     2831
 struct SplitCost {
   int resident;   // blocks that an SM holds
   int64_t least;  // tokens of a range, at least
