@@ -29,8 +29,8 @@ namespace {
 
 thread_local char g_last_cuda_error[256] = "";
 
-// Notes the error and takes it out of the runtime, which would hand it to the
-// next check behind a launch, here or in the caller's own code.
+// Notes the error and takes it out of the (statically linked) runtime, which would
+// hand it to the check behind the next call's launch.
 kda_status_t cuda_fail(cudaError_t e) {
   cudaGetLastError();
   std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s", cudaGetErrorName(e),
